@@ -25,12 +25,16 @@ EXPORTS = ["lq_block_bytes", "lq_block_elems", "lq_row_bytes", "lq_status_str", 
            "lq_qkv_mixed_rmsnorm", "lq_pack_gate_up", "lq_ffn_gate_up_act", "lq_ffn_gate_up_act_rmsnorm",
            "lq_ffn", "lq_moe_workspace_bytes", "lq_moe_ffn", "lq_moe_ffn_ex_workspace_bytes", "lq_moe_ffn_ex",
            "lq_moe_ffn_static",
+           "lq_rope", "lq_kv8_append", "lq_kv8_attn_workspace_bytes", "lq_kv8_attn", "lq_kv_reserve", "lq_kv_fork",
+           "lq_kv_release", "lq_kv_compact", "lq_kv8_copy_pages",
            "lq_device_status",
            "lq_set_wait_timeout_ns", "lq_probe_timeout"]
 
 LQ_MOE_STATIC_SCRATCH_BYTES = 4 << 20
 LQ_MOE_MAX_SHARED = 16
 LQ_GEMM_MIN_M = 32
+LQ_ROPE_HALF, LQ_ROPE_ADJACENT = 1, 2
+LQ_STATUS_TIMEOUT, LQ_STATUS_BADARG = 1, 2
 
 
 class LqError(RuntimeError):
@@ -79,6 +83,16 @@ def lib():
             "lq_moe_ffn_ex": ([vp, i32, i32, i32, i32, vp, vp, vp, i64, i64, i32, vp, vp, vp, i64, vp, vp, vp, i32,
                                vp, vp, vp, sz, vp], i32),
             "lq_moe_ffn_static": ([vp, i32, i32, i32, vp, vp, vp, i64, i64, vp, vp, i32, vp, vp, vp], i32),
+            "lq_rope": ([vp, i32, i64, vp, i64, vp, i32, i64, vp, i64, i32, i32, i32, vp, i32, vp, vp, i32, vp], i32),
+            "lq_kv8_append": ([vp, vp, i32, vp, vp, i32, vp, i64, vp, i64, i32, vp], i32),
+            "lq_kv8_attn_workspace_bytes": ([i32, i32, i32, i32, i32], sz),
+            "lq_kv8_attn": ([vp, vp, i32, vp, vp, i32, vp, i32, i64, i32, C.c_float, C.c_float, i32, vp, vp, vp, i64, vp,
+                             sz, vp], i32),
+            "lq_kv_reserve": ([vp, i32, vp, i32, i32, vp, vp, i32, vp, vp], i32),
+            "lq_kv_fork": ([vp, i32, i32, vp, i32, i32, vp, vp, vp, i32, vp, vp, vp, vp], i32),
+            "lq_kv_release": ([vp, i32, i32, vp, i32, vp, vp, i32, vp], i32),
+            "lq_kv_compact": ([vp, i32, i32, vp, i32, vp, vp, vp, vp, vp], i32),
+            "lq_kv8_copy_pages": ([vp, i32, vp, vp, i32, vp, vp], i32),
             "lq_device_status": ([vp, C.POINTER(C.c_uint32)], i32),
             "lq_set_wait_timeout_ns": ([u64], None),
             "lq_probe_timeout": ([u64, vp], i32),
@@ -252,6 +266,64 @@ def lq_moe_ffn_static(router, n_experts, topk, fmt, W1, W3, W2, hidden, inter, X
                                           C.cast(a3, C.c_void_p), C.cast(a2, C.c_void_p), hidden, inter,
                                           _ptr(X), _ptr(Y), ntok, _ptr(topk_idx), _ptr(topk_w),
                                           _stream(stream)))
+
+
+class LqKv8(C.Structure):
+    """lq_kv8: one layer's 8-bit KV cache.  Holds its tensors, so it keeps them alive."""
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("n_pages", C.c_int64), ("n_kv", C.c_int32), ("page", C.c_int32), ("head_dim", C.c_int32)]
+
+    def __init__(self, k, v, k_scale, v_scale, n_pages, n_kv, page, head_dim):
+        super().__init__(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), n_pages, n_kv, page, head_dim)
+        self.tensors = (k, v, k_scale, v_scale)
+
+
+def lq_rope(q, n_q, ld_q, q_out, ld_qo, k, n_k, ld_k, k_out, ld_ko, head_dim, rot_dim, pairing, pos, n_axes, axis, freq,
+            ntok, stream=None):
+    return _check(lib().lq_rope(_ptr(q), n_q, ld_q, _ptr(q_out), ld_qo, _ptr(k), n_k, ld_k, _ptr(k_out), ld_ko,
+                                head_dim, rot_dim, pairing, _ptr(pos), n_axes, _ptr(axis), _ptr(freq), ntok,
+                                _stream(stream)))
+
+
+def lq_kv8_append(cache, table, max_pages, start, cu, nseq, k, ld_k, v, ld_v, ntok, stream=None):
+    return _check(lib().lq_kv8_append(C.addressof(cache), _ptr(table), max_pages, _ptr(start), _ptr(cu), nseq, _ptr(k),
+                                      ld_k, _ptr(v), ld_v, ntok, _stream(stream)))
+
+
+def lq_kv8_attn_workspace_bytes(n_q, n_kv, head_dim, nseq, ntok) -> int:
+    return lib().lq_kv8_attn_workspace_bytes(n_q, n_kv, head_dim, nseq, ntok)
+
+
+def lq_kv8_attn(cache, table, max_pages, start, cu, nseq, q, n_q, ld_q, ntok, scale, softcap, window, prefix, slopes,
+                out, ld_out, workspace=None, ws_bytes=0, stream=None):
+    return _check(lib().lq_kv8_attn(C.addressof(cache), _ptr(table), max_pages, _ptr(start), _ptr(cu), nseq, _ptr(q), n_q,
+                                    ld_q, ntok, scale, softcap, window, _ptr(prefix), _ptr(slopes), _ptr(out), ld_out,
+                                    _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def lq_kv_reserve(table, max_pages, ref, n_pages, page, start, cu, nseq, info, stream=None):
+    return _check(lib().lq_kv_reserve(_ptr(table), max_pages, _ptr(ref), n_pages, page, _ptr(start), _ptr(cu), nseq,
+                                      _ptr(info), _stream(stream)))
+
+
+def lq_kv_fork(table, n_rows, max_pages, ref, n_pages, page, lens, parent, child, n, src, dst, info, stream=None):
+    return _check(lib().lq_kv_fork(_ptr(table), n_rows, max_pages, _ptr(ref), n_pages, page, _ptr(lens), _ptr(parent),
+                                   _ptr(child), n, _ptr(src), _ptr(dst), _ptr(info), _stream(stream)))
+
+
+def lq_kv_release(table, n_rows, max_pages, ref, n_pages, lens, rows, n, stream=None):
+    return _check(lib().lq_kv_release(_ptr(table), n_rows, max_pages, _ptr(ref), n_pages, _ptr(lens), _ptr(rows), n,
+                                      _stream(stream)))
+
+
+def lq_kv_compact(table, n_rows, max_pages, ref, n_pages, map, src, dst, info, stream=None):
+    return _check(lib().lq_kv_compact(_ptr(table), n_rows, max_pages, _ptr(ref), n_pages, _ptr(map), _ptr(src), _ptr(dst),
+                                      _ptr(info), _stream(stream)))
+
+
+def lq_kv8_copy_pages(layers, src, dst, n, count=None, stream=None):
+    arr = (C.c_void_p * len(layers))(*[C.addressof(c) for c in layers])
+    return _check(lib().lq_kv8_copy_pages(arr, len(layers), _ptr(src), _ptr(dst), n, _ptr(count), _stream(stream)))
 
 
 def lq_device_status(stream=None):

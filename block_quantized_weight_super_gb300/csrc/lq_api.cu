@@ -152,6 +152,33 @@ int dev_info(DevInfo** out) {
     return LQ_OK;
 }
 
+}  // namespace
+
+// The same for the entry points of other files (lq_internal.h).
+int api_fail(int code, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return code;
+}
+
+int api_cuda_fail(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+
+void api_clear() { g_err[0] = 0; }
+
+int api_device(ApiDevice* out) {
+    DevInfo* d = nullptr;
+    const int rc = dev_info(&d);
+    if (rc != LQ_OK) return rc;
+    out->sms = d->sms;
+    out->status = d->status;
+    out->timeout_ns = g_timeout_ns.load();
+    return LQ_OK;
+}
+
+namespace {
+
 // ---------------------------------------------------------------- planning
 struct QPlan {
     int B = 0, R = 0, NC = 0, RT = 0, ipt = 0, nstages = 0, stage_bytes = 0;

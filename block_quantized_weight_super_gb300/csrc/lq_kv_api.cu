@@ -1,0 +1,310 @@
+// lq_kv_api.cu -- the C entry points of rotary positions, the 8-bit KV cache,
+// its attention and its pages: argument validation and dispatch.  Host code
+// only.
+#include <cmath>
+
+#include "../../include/lq.h"
+#include "lq_internal.h"
+#include "lq_kv.cuh"
+
+using namespace lq;
+
+namespace {
+
+bool al(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int check_ptr(const void* p, uintptr_t a, const char* name) {
+    if (!p) return api_fail(LQ_EINVAL, "%s is null", name);
+    if (!al(p, a)) return api_fail(LQ_EALIGN, "%s not %d-byte aligned", name, (int)a);
+    return LQ_OK;
+}
+
+// log2(page), or -1
+int page_shift(int page) {
+    for (int s = 4; s <= 8; ++s)
+        if (page == 1 << s) return s;
+    return -1;
+}
+
+int check_cache(const lq_kv8* c, KvView& v) {
+    if (!c) return api_fail(LQ_EINVAL, "cache is null");
+    if (c->n_pages < 1 || c->n_pages > INT32_MAX || c->n_kv < 1 || c->n_kv > 1024)
+        return api_fail(LQ_ESHAPE, "cache: n_pages %lld n_kv %d", (long long)c->n_pages, (int)c->n_kv);
+    const int s = page_shift(c->page);
+    if (s < 0) return api_fail(LQ_ESHAPE, "cache: page %d (16, 32, 64, 128 or 256)", (int)c->page);
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+        return api_fail(LQ_ESHAPE, "cache: head_dim %d (64, 128 or 256)", (int)c->head_dim);
+    int rc;
+    if ((rc = check_ptr(c->k, 16, "cache.k")) || (rc = check_ptr(c->v, 16, "cache.v")) ||
+        (rc = check_ptr(c->k_scale, 4, "cache.k_scale")) || (rc = check_ptr(c->v_scale, 4, "cache.v_scale")))
+        return rc;
+    v.k = static_cast<int8_t*>(c->k);
+    v.v = static_cast<int8_t*>(c->v);
+    v.ks = c->k_scale;
+    v.vs = c->v_scale;
+    v.n_pages = c->n_pages;
+    v.n_kv = c->n_kv;
+    v.pshift = s;
+    v.d = c->head_dim;
+    return LQ_OK;
+}
+
+int check_step(const int32_t* table, int max_pages, const int32_t* start, const int32_t* cu, int nseq, int ntok,
+               KvStep& s) {
+    if (nseq < 0 || nseq > 65535) return api_fail(LQ_ESHAPE, "nseq %d (at most 65535)", nseq);
+    if (ntok < 0 || ntok > 1 << 24) return api_fail(LQ_ESHAPE, "ntok %d (at most 2^24)", ntok);
+    if (max_pages < 1) return api_fail(LQ_ESHAPE, "max_pages %d", max_pages);
+    if (!cu && ntok != nseq) return api_fail(LQ_EINVAL, "cu is null but ntok %d differs from nseq %d", ntok, nseq);
+    if (nseq == 0 && ntok != 0) return api_fail(LQ_EINVAL, "ntok %d without sequences", ntok);
+    if (ntok == 0) return LQ_OK;         // nothing to do (an empty tensor has no address)
+    int rc;
+    if ((rc = check_ptr(table, 4, "table")) || (rc = check_ptr(start, 4, "start"))) return rc;
+    if (cu && (rc = check_ptr(cu, 4, "cu"))) return rc;
+    s.table = table;
+    s.start = start;
+    s.cu = cu;
+    s.max_pages = max_pages;
+    s.nseq = nseq;
+    s.ntok = ntok;
+    return LQ_OK;
+}
+
+int check_rows(const void* p, int64_t ld, int64_t width, const char* name) {
+    int rc = check_ptr(p, 4, name);
+    if (rc) return rc;
+    if (ld < width || ld > INT64_C(1) << 40)
+        return api_fail(LQ_ESHAPE, "%s: ld %lld below its width %lld", name, (long long)ld, (long long)width);
+    return LQ_OK;
+}
+
+int check_pages(const int32_t* table, int max_pages, const int32_t* ref, int n_pages) {
+    if (max_pages < 1 || n_pages < 1) return api_fail(LQ_ESHAPE, "max_pages %d n_pages %d", max_pages, n_pages);
+    int rc;
+    if ((rc = check_ptr(table, 4, "table")) || (rc = check_ptr(ref, 4, "ref"))) return rc;
+    return LQ_OK;
+}
+
+int launched(cudaError_t e, const char* what) { return e == cudaSuccess ? LQ_OK : api_cuda_fail(e, what); }
+
+cudaStream_t stream_of(lq_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
+
+}  // namespace
+
+extern "C" {
+
+int lq_rope(const float* q, int n_q, int64_t ld_q, float* q_out, int64_t ld_qo, const float* k, int n_k, int64_t ld_k,
+            float* k_out, int64_t ld_ko, int head_dim, int rot_dim, int pairing, const int32_t* pos, int n_axes,
+            const uint8_t* axis, const double* freq, int ntok, lq_stream_t stream) {
+    api_clear();
+    if (n_q < 1 || n_q > 65535 || n_k < 0 || n_k > 65535) return api_fail(LQ_ESHAPE, "heads %d, %d", n_q, n_k);
+    if (head_dim < 2 || head_dim > 1024 || rot_dim < 2 || rot_dim > head_dim || rot_dim % 2)
+        return api_fail(LQ_ESHAPE, "head_dim %d rot_dim %d", head_dim, rot_dim);
+    if (pairing != LQ_ROPE_HALF && pairing != LQ_ROPE_ADJACENT) return api_fail(LQ_EINVAL, "pairing %d", pairing);
+    if (n_axes < 1 || n_axes > 255) return api_fail(LQ_EINVAL, "n_axes %d", n_axes);
+    if (ntok < 0) return api_fail(LQ_ESHAPE, "ntok %d", ntok);
+    if (ntok == 0) return LQ_OK;         // (an empty tensor has no address)
+    int rc;
+    if ((rc = check_rows(q, ld_q, (int64_t)n_q * head_dim, "q")) ||
+        (rc = check_rows(q_out, ld_qo, (int64_t)n_q * head_dim, "q_out")))
+        return rc;
+    if (n_k > 0 && ((rc = check_rows(k, ld_k, (int64_t)n_k * head_dim, "k")) ||
+                    (rc = check_rows(k_out, ld_ko, (int64_t)n_k * head_dim, "k_out"))))
+        return rc;
+    if ((q == q_out && ld_q != ld_qo) || (n_k > 0 && k == k_out && ld_k != ld_ko))
+        return api_fail(LQ_EINVAL, "in place with another ld");
+    if ((rc = check_ptr(pos, 4, "pos")) || (rc = check_ptr(freq, 8, "freq"))) return rc;
+    RopeParams P{};
+    P.q = q;
+    P.k = k;
+    P.qo = q_out;
+    P.ko = k_out;
+    P.ld_q = ld_q;
+    P.ld_k = ld_k;
+    P.ld_qo = ld_qo;
+    P.ld_ko = ld_ko;
+    P.n_q = n_q;
+    P.n_k = n_k;
+    P.d = head_dim;
+    P.rot = rot_dim;
+    P.adjacent = pairing == LQ_ROPE_ADJACENT;
+    P.pos = pos;
+    P.n_axes = n_axes;
+    P.axis = axis;
+    P.freq = freq;
+    P.ntok = ntok;
+    ApiDevice d;
+    if ((rc = api_device(&d))) return rc;
+    P.status = d.status;
+    return launched(launch_rope(P, d.sms, stream_of(stream)), "rope launch");
+}
+
+int lq_kv8_append(const lq_kv8* cache, const int32_t* table, int max_pages, const int32_t* start, const int32_t* cu,
+                  int nseq, const float* k, int64_t ld_k, const float* v, int64_t ld_v, int ntok, lq_stream_t stream) {
+    api_clear();
+    KvView c;
+    KvStep s;
+    int rc;
+    if ((rc = check_cache(cache, c)) || (rc = check_step(table, max_pages, start, cu, nseq, ntok, s))) return rc;
+    if (ntok == 0) return LQ_OK;
+    const int64_t w = (int64_t)c.n_kv * c.d;
+    if ((rc = check_rows(k, ld_k, w, "k")) || (rc = check_rows(v, ld_v, w, "v"))) return rc;
+    ApiDevice d;
+    if ((rc = api_device(&d))) return rc;
+    return launched(launch_kv8_append(c, s, k, ld_k, v, ld_v, d.status, stream_of(stream)), "kv8 append launch");
+}
+
+size_t lq_kv8_attn_workspace_bytes(int n_q, int n_kv, int head_dim, int nseq, int ntok) {
+    if (n_q < 1 || n_kv < 1 || n_q % n_kv || nseq < 0 || ntok < 0 ||
+        (head_dim != 64 && head_dim != 128 && head_dim != 256))
+        return 0;
+    return kv8_attn_workspace(n_q, n_kv, head_dim, nseq, ntok);
+}
+
+int lq_kv8_attn(const lq_kv8* cache, const int32_t* table, int max_pages, const int32_t* start, const int32_t* cu,
+                int nseq, const float* q, int n_q, int64_t ld_q, int ntok, float scale, float softcap, int window,
+                const int32_t* prefix, const float* slopes, float* out, int64_t ld_out, void* workspace,
+                size_t ws_bytes, lq_stream_t stream) {
+    api_clear();
+    KvView c;
+    KvStep s;
+    int rc;
+    if ((rc = check_cache(cache, c)) || (rc = check_step(table, max_pages, start, cu, nseq, ntok, s))) return rc;
+    if (n_q < 1 || n_q > 65535 || n_q % c.n_kv)
+        return api_fail(LQ_ESHAPE, "n_q %d is no multiple of n_kv %d", n_q, (int)c.n_kv);
+    if (!std::isfinite(scale)) return api_fail(LQ_EINVAL, "scale %g", (double)scale);
+    if (!(softcap >= 0.f) || !std::isfinite(softcap)) return api_fail(LQ_EINVAL, "softcap %g", (double)softcap);
+    if (window < 0) return api_fail(LQ_EINVAL, "window %d", window);
+    if (ntok == 0) return LQ_OK;
+    const int64_t w = (int64_t)n_q * c.d;
+    if ((rc = check_rows(q, ld_q, w, "q")) || (rc = check_rows(out, ld_out, w, "out"))) return rc;
+    if (prefix && (rc = check_ptr(prefix, 4, "prefix"))) return rc;
+    if (slopes && (rc = check_ptr(slopes, 4, "slopes"))) return rc;
+    const size_t need = kv8_attn_workspace(n_q, c.n_kv, c.d, nseq, ntok);
+    if (!workspace || ws_bytes < need)
+        return api_fail(LQ_EWORKSPACE, "workspace %zu bytes, needs %zu", workspace ? ws_bytes : (size_t)0, need);
+    if (!al(workspace, 256)) return api_fail(LQ_EALIGN, "workspace not 256-byte aligned");
+    AttnParams P{};
+    P.c = c;
+    P.s = s;
+    P.q = q;
+    P.out = out;
+    P.ld_q = ld_q;
+    P.ld_out = ld_out;
+    P.n_q = n_q;
+    P.scale = scale;
+    P.softcap = softcap;
+    P.window = window;
+    P.prefix = prefix;
+    P.slopes = slopes;
+    P.ws = static_cast<uint8_t*>(workspace);
+    ApiDevice d;
+    if ((rc = api_device(&d))) return rc;
+    P.status = d.status;
+    P.timeout_ns = d.timeout_ns;
+    return launched(launch_kv8_attn(P, d.sms, stream_of(stream)), "kv8 attention launch");
+}
+
+int lq_kv_reserve(int32_t* table, int max_pages, int32_t* ref, int n_pages, int page, const int32_t* start,
+                  const int32_t* cu, int nseq, int32_t* info, lq_stream_t stream) {
+    api_clear();
+    int rc;
+    if ((rc = check_pages(table, max_pages, ref, n_pages)) || (rc = check_ptr(start, 4, "start")) ||
+        (rc = check_ptr(info, 4, "info")))
+        return rc;
+    if (cu && (rc = check_ptr(cu, 4, "cu"))) return rc;
+    if (page_shift(page) < 0) return api_fail(LQ_ESHAPE, "page %d", page);
+    if (nseq < 0 || nseq > 8192) return api_fail(LQ_ESHAPE, "nseq %d (at most 8192)", nseq);
+    if (nseq == 0) return LQ_OK;
+    return launched(launch_kv_reserve(table, max_pages, ref, n_pages, page_shift(page), start, cu, nseq, info,
+                                      stream_of(stream)),
+                    "kv reserve launch");
+}
+
+int lq_kv_fork(int32_t* table, int n_rows, int max_pages, int32_t* ref, int n_pages, int page, int32_t* lens,
+               const int32_t* parent, const int32_t* child, int n, int32_t* src, int32_t* dst, int32_t* info,
+               lq_stream_t stream) {
+    api_clear();
+    int rc;
+    if ((rc = check_pages(table, max_pages, ref, n_pages)) || (rc = check_ptr(lens, 4, "lens")) ||
+        (rc = check_ptr(parent, 4, "parent")) || (rc = check_ptr(child, 4, "child")) || (rc = check_ptr(src, 4, "src")) ||
+        (rc = check_ptr(dst, 4, "dst")) || (rc = check_ptr(info, 4, "info")))
+        return rc;
+    if (page_shift(page) < 0) return api_fail(LQ_ESHAPE, "page %d", page);
+    if (n_rows < 1) return api_fail(LQ_ESHAPE, "n_rows %d", n_rows);
+    if (n < 0 || n > 4096) return api_fail(LQ_ESHAPE, "n %d (at most 4096)", n);
+    if (n == 0) return LQ_OK;
+    ApiDevice d;
+    if ((rc = api_device(&d))) return rc;
+    return launched(launch_kv_fork(table, n_rows, max_pages, ref, n_pages, page_shift(page), lens, parent, child, n, src,
+                                   dst, info, d.status, stream_of(stream)),
+                    "kv fork launch");
+}
+
+int lq_kv_release(int32_t* table, int n_rows, int max_pages, int32_t* ref, int n_pages, int32_t* lens,
+                  const int32_t* rows, int n, lq_stream_t stream) {
+    api_clear();
+    int rc;
+    if ((rc = check_pages(table, max_pages, ref, n_pages)) || (rc = check_ptr(rows, 4, "rows"))) return rc;
+    if (lens && (rc = check_ptr(lens, 4, "lens"))) return rc;
+    if (n_rows < 1 || n < 0) return api_fail(LQ_ESHAPE, "n_rows %d n %d", n_rows, n);
+    if (n == 0) return LQ_OK;
+    ApiDevice d;
+    if ((rc = api_device(&d))) return rc;
+    return launched(launch_kv_release(table, n_rows, max_pages, ref, n_pages, lens, rows, n, d.status, stream_of(stream)),
+                    "kv release launch");
+}
+
+int lq_kv_compact(int32_t* table, int n_rows, int max_pages, int32_t* ref, int n_pages, int32_t* map, int32_t* src,
+                  int32_t* dst, int32_t* info, lq_stream_t stream) {
+    api_clear();
+    int rc;
+    if ((rc = check_pages(table, max_pages, ref, n_pages)) || (rc = check_ptr(map, 4, "map")) ||
+        (rc = check_ptr(info, 4, "info")))
+        return rc;
+    if (n_pages > 1 && ((rc = check_ptr(src, 4, "src")) || (rc = check_ptr(dst, 4, "dst")))) return rc;
+    if (n_rows < 0) return api_fail(LQ_ESHAPE, "n_rows %d", n_rows);
+    ApiDevice d;
+    if ((rc = api_device(&d))) return rc;
+    return launched(launch_kv_compact(table, n_rows, max_pages, ref, n_pages, map, src, dst, info, d.status,
+                                      stream_of(stream)),
+                    "kv compact launch");
+}
+
+int lq_kv8_copy_pages(const lq_kv8* const* layers, int n_layers, const int32_t* src, const int32_t* dst, int n,
+                      const int32_t* count, lq_stream_t stream) {
+    api_clear();
+    if (!layers) return api_fail(LQ_EINVAL, "layers is null");
+    if (n_layers < 0 || n < 0) return api_fail(LQ_ESHAPE, "n_layers %d n %d", n_layers, n);
+    int rc;
+    if ((rc = check_ptr(src, 4, "src")) || (rc = check_ptr(dst, 4, "dst"))) return rc;
+    if (count && (rc = check_ptr(count, 4, "count"))) return rc;
+    KvView a{}, b;
+    for (int l = 0; l < n_layers; ++l) {
+        if ((rc = check_cache(layers[l], b))) return rc;
+        if (l == 0) a = b;
+        if (b.n_pages != a.n_pages || b.n_kv != a.n_kv || b.pshift != a.pshift || b.d != a.d)
+            return api_fail(LQ_ESHAPE, "layer %d has another shape than layer 0", l);
+    }
+    if (n == 0 || n_layers == 0) return LQ_OK;
+    ApiDevice d;
+    if ((rc = api_device(&d))) return rc;
+    const int64_t units = ((int64_t)a.n_kv * a.d << a.pshift) / 16;
+    for (int l0 = 0; l0 < n_layers; l0 += KV_MAX_LAYERS) {
+        KvLayers L{};
+        const int m = n_layers - l0 < KV_MAX_LAYERS ? n_layers - l0 : KV_MAX_LAYERS;
+        for (int l = 0; l < m; ++l) {
+            const lq_kv8* c = layers[l0 + l];
+            L.k[l] = static_cast<int8_t*>(c->k);
+            L.v[l] = static_cast<int8_t*>(c->v);
+            L.ks[l] = c->k_scale;
+            L.vs[l] = c->v_scale;
+        }
+        if ((rc = launched(launch_kv8_copy(L, m, src, dst, n, count, a.n_pages, a.n_kv, units, d.status,
+                                           stream_of(stream)),
+                           "kv8 copy launch")))
+            return rc;
+    }
+    return LQ_OK;
+}
+
+}  // extern "C"

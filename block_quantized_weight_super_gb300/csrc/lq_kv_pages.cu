@@ -1,0 +1,336 @@
+// lq_kv_pages.cu -- the bookkeeping of the cache's pages: reserve, fork,
+// release, compact.  All of it is integers with one right answer: new pages are
+// the free ones of lowest index in ascending order, dealt out in sequence
+// order, so no atomic decides anything (the only ones add to reference
+// counts, whose order does not matter).
+//
+// Dealing out needs the rank of every free page and of every request.  One
+// block of 1024 threads walks the pool in tiles of 4096 reference counts with
+// a block-wide prefix sum per tile, first to see whether the pool has enough
+// free pages (nothing is changed otherwise), then to hand them out; it stops
+// at the last page needed.  A tile costs about a microsecond, and a request
+// is found by bisection of the requests' prefix sums in shared memory.
+#include "lq_internal.h"
+#include "lq_kv.cuh"
+
+namespace lq {
+namespace {
+
+constexpr int PG_THREADS = 1024, PG_PER = 4, PG_TILE = PG_THREADS * PG_PER;
+
+// Exclusive prefix sum over the block; `total` gets the sum.
+__device__ __forceinline__ int block_scan(int v, int* red, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, s, o);
+        if (lane >= o) s += u;
+    }
+    if (lane == 31) red[warp] = s;
+    __syncthreads();
+    if (warp == 0) {
+        int r = red[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, r, o);
+            if (lane >= o) r += u;
+        }
+        red[lane] = r;
+    }
+    __syncthreads();
+    const int before = warp ? red[warp - 1] : 0;
+    total = red[31];
+    __syncthreads();
+    return before + s - v;
+}
+
+// off[i] = sum of off[0 .. i) in place, off[n] the whole sum (returned).
+__device__ int scan_requests(int* off, int n, int* red) {
+    int run = 0;
+    for (int i0 = 0; i0 < n; i0 += PG_THREADS) {
+        const int i = i0 + threadIdx.x;
+        int total;
+        const int e = block_scan(i < n ? off[i] : 0, red, total);
+        if (i < n) off[i] = run + e;
+        run += total;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) off[n] = run;
+    __syncthreads();
+    return run;
+}
+
+// Walks the free pages in ascending order, f(rank, page) for the first
+// `want`; returns how many there are (at most `want` counted exactly).
+template <class F>
+__device__ int walk_free(const int32_t* ref, int n_pages, int want, int* red, F f) {
+    int run = 0;
+    for (int p0 = 0; p0 < n_pages && run < want; p0 += PG_TILE) {
+        const int p = p0 + PG_PER * threadIdx.x;
+        bool fr[PG_PER];
+        int c = 0;
+#pragma unroll
+        for (int e = 0; e < PG_PER; ++e) {
+            fr[e] = p + e < n_pages && ref[p + e] == 0;
+            c += fr[e];
+        }
+        int total, r = run + block_scan(c, red, total);
+#pragma unroll
+        for (int e = 0; e < PG_PER; ++e)
+            if (fr[e]) {
+                if (r < want) f(r, p + e);
+                ++r;
+            }
+        run += total;
+    }
+    return run;
+}
+
+// A sequence's request: its first missing entry and how many follow.  The
+// entries of the step's positions must be held up to some point and missing
+// from there on.
+__global__ void __launch_bounds__(PG_THREADS) kv_reserve_kernel(int32_t* table, int max_pages, int32_t* ref, int n_pages,
+                                                                int pshift, const int32_t* start, const int32_t* cu,
+                                                                int nseq, int32_t* info) {
+    extern __shared__ int sh[];
+    int* off = sh;                  // [nseq + 1]
+    int* first = sh + nseq + 1;     // [nseq]
+    __shared__ int red[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int bad = 0;
+    for (int s = warp; s < nseq; s += PG_THREADS / 32) {
+        const int n = cu ? cu[s + 1] - cu[s] : 1;
+        const int64_t end = (int64_t)start[s] + n, p0 = max(start[s], 0);
+        const int64_t j0 = p0 >> pshift, j1 = n > 0 && end > p0 ? ((end - 1) >> pshift) + 1 : j0;
+        int miss = 0, f = INT32_MAX;
+        if (n < 0 || j1 > max_pages) {
+            bad = j1 > j0 || n < 0;
+        } else {
+            for (int64_t j = j0 + lane; j < j1; j += 32)
+                if (table[(int64_t)s * max_pages + j] < 0) {
+                    ++miss;
+                    f = min(f, (int)j);
+                }
+            miss = __reduce_add_sync(0xFFFFFFFFu, miss);
+            f = __reduce_min_sync(0xFFFFFFFFu, f);
+            if (miss > 0 && miss != (int)(j1 - f)) bad = 1;
+        }
+        if (lane == 0) {
+            off[s] = miss;
+            first[s] = f;
+        }
+    }
+    bad = __syncthreads_or(bad);
+    const int want = scan_requests(off, nseq, red);
+    const int have = bad ? 0 : walk_free(ref, n_pages, want, red, [](int, int) {});
+    if (tid == 0) {
+        info[0] = bad || have >= want ? 0 : want - have;
+        info[1] = bad ? 1 : 0;
+    }
+    if (bad || have < want) return;
+    walk_free(ref, n_pages, want, red, [&](int r, int p) {
+        const int s = kv_find(nseq, r, [&](int i) { return off[i]; });
+        table[(int64_t)s * max_pages + first[s] + (r - off[s])] = p;
+        ref[p] = 1;
+    });
+}
+
+// The new last pages of the children (off: the rank of each request).
+__global__ void __launch_bounds__(PG_THREADS) kv_fork_kernel(const int32_t* table, int n_rows, int max_pages, int32_t* ref,
+                                                             int n_pages, int pshift, const int32_t* lens,
+                                                             const int32_t* parent, const int32_t* child, int n,
+                                                             int32_t* src, int32_t* dst, int32_t* info) {
+    extern __shared__ int off[];    // [n + 1]
+    __shared__ int red[32];
+    const int tid = threadIdx.x, P = 1 << pshift;
+    int bad = 0;
+    for (int i = tid; i < n; i += PG_THREADS) {
+        const int a = parent[i], b = child[i];
+        int tail = 0, from = -1;
+        if (a < 0 || a >= n_rows || b < 0 || b >= n_rows) {
+            bad = 1;
+        } else {
+            const int64_t len = lens[a];
+            if (len < 0 || len > (int64_t)max_pages << pshift) {
+                bad = 1;
+            } else if (len & (P - 1)) {
+                tail = 1;
+                from = table[(int64_t)a * max_pages + (len >> pshift)];
+                if (from < 0 || from >= n_pages) bad = 1;
+            }
+        }
+        off[i] = tail;
+        src[i] = from;
+        dst[i] = -1;
+    }
+    bad = __syncthreads_or(bad);
+    const int want = scan_requests(off, n, red);
+    const int have = bad ? 0 : walk_free(ref, n_pages, want, red, [](int, int) {});
+    if (tid == 0) {
+        info[0] = bad || have >= want ? 0 : want - have;
+        info[1] = bad ? 1 : 0;
+    }
+    if (bad || have < want) {
+        for (int i = tid; i < n; i += PG_THREADS) src[i] = -1;
+        return;
+    }
+    walk_free(ref, n_pages, want, red, [&](int r, int p) {
+        // the last request of this rank is the one that takes it: those
+        // before it with the same prefix sum ask for nothing
+        dst[kv_find(n, r, [&](int i) { return off[i]; })] = p;
+        ref[p] = 1;
+    });
+}
+
+// Row child[i]: the parent's full pages, the new page, -1 behind them.
+__global__ void __launch_bounds__(128) kv_fork_rows_kernel(int32_t* table, int max_pages, int32_t* ref, int n_pages,
+                                                           int pshift, int32_t* lens, const int32_t* parent,
+                                                           const int32_t* child, const int32_t* dst, const int32_t* info,
+                                                           unsigned* status) {
+    if (info[0] != 0 || info[1] != 0) return;
+    const int i = blockIdx.x;
+    const int64_t a = parent[i], b = child[i];
+    const int len = lens[a], full = len >> pshift;
+    for (int j = threadIdx.x; j < max_pages; j += 128) {
+        int p = -1;
+        if (j < full) {
+            p = table[a * max_pages + j];
+            if (p < 0 || p >= n_pages) {
+                record_status(status, STATUS_BADARG);
+                p = -1;
+            } else {
+                atomicAdd(ref + p, 1);
+            }
+        } else if (j == full) {
+            p = dst[i];
+        }
+        table[b * max_pages + j] = p;
+    }
+    if (threadIdx.x == 0) lens[b] = len;
+}
+
+__global__ void __launch_bounds__(128) kv_release_kernel(int32_t* table, int n_rows, int max_pages, int32_t* ref,
+                                                         int n_pages, int32_t* lens, const int32_t* rows,
+                                                         unsigned* status) {
+    const int64_t r = rows[blockIdx.x];
+    if (r < 0 || r >= n_rows) {
+        if (threadIdx.x == 0) record_status(status, STATUS_BADARG);
+        return;
+    }
+    for (int j = threadIdx.x; j < max_pages; j += 128) {
+        const int p = atomicExch(table + r * max_pages + j, -1);   // a row named twice gives its pages back once
+        if (p < 0) continue;
+        if (p >= n_pages || atomicSub(ref + p, 1) <= 0) {          // no row can hold a page of count 0
+            if (p < n_pages) atomicAdd(ref + p, 1);
+            record_status(status, STATUS_BADARG);
+        }
+    }
+    if (lens && threadIdx.x == 0) lens[r] = 0;
+}
+
+// src, dst, map and the new reference counts.  Used pages at or above u and
+// free ones below it are equally many (u = the number of used pages).
+__global__ void __launch_bounds__(PG_THREADS) kv_compact_kernel(int32_t* ref, int n_pages, int32_t* map, int32_t* src,
+                                                                int32_t* dst, int32_t* info) {
+    __shared__ int red[32];
+    const int tid = threadIdx.x;
+    int c = 0, u;
+    for (int p = tid; p < n_pages; p += PG_THREADS) c += ref[p] > 0;
+    block_scan(c, red, u);
+    int nh = 0, nl = 0;
+    for (int p0 = 0; p0 < n_pages; p0 += PG_TILE) {
+        const int p = p0 + PG_PER * tid;
+        int kind[PG_PER], both = 0;          // 1: a used page that moves, 2: a free one that takes it
+#pragma unroll
+        for (int e = 0; e < PG_PER; ++e) {
+            kind[e] = 0;
+            if (p + e < n_pages) {
+                const bool used = ref[p + e] > 0;
+                kind[e] = used && p + e >= u ? 1 : !used && p + e < u ? 2 : 0;
+                map[p + e] = used && p + e < u ? p + e : -1;
+            }
+            both += kind[e] == 1 ? 1 : kind[e] == 2 ? 1 << 16 : 0;      // two counts of a tile, each at most 4096
+        }
+        int total;
+        const int at = block_scan(both, red, total);
+        int h = nh + (at & 0xFFFF), l = nl + (at >> 16);
+#pragma unroll
+        for (int e = 0; e < PG_PER; ++e) {
+            if (kind[e] == 1) src[h++] = p + e;
+            if (kind[e] == 2) dst[l++] = p + e;
+        }
+        nh += total & 0xFFFF;
+        nl += total >> 16;
+    }
+    __syncthreads();
+    for (int i = tid; i < n_pages / 2; i += PG_THREADS) {
+        if (i < nh) {
+            const int a = src[i], b = dst[i];
+            map[a] = b;
+            ref[b] = ref[a];
+            ref[a] = 0;
+        } else {
+            src[i] = -1;
+            dst[i] = -1;
+        }
+    }
+    if (tid == 0) {
+        info[0] = nh;
+        info[1] = 0;
+    }
+}
+
+__global__ void __launch_bounds__(256) kv_remap_kernel(int32_t* table, int64_t n, const int32_t* map, int n_pages,
+                                                       unsigned* status) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int p = table[i];
+        if (p < 0) continue;
+        if (p >= n_pages) record_status(status, STATUS_BADARG);
+        else table[i] = map[p];
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_reserve(int32_t* table, int max_pages, int32_t* ref, int n_pages, int pshift, const int32_t* start,
+                              const int32_t* cu, int nseq, int32_t* info, cudaStream_t st) {
+    const size_t smem = (2 * (size_t)nseq + 1) * sizeof(int);
+    if (smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(kv_reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    kv_reserve_kernel<<<1, PG_THREADS, smem, st>>>(table, max_pages, ref, n_pages, pshift, start, cu, nseq, info);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_fork(int32_t* table, int n_rows, int max_pages, int32_t* ref, int n_pages, int pshift,
+                           int32_t* lens, const int32_t* parent, const int32_t* child, int n, int32_t* src, int32_t* dst,
+                           int32_t* info, unsigned* status, cudaStream_t st) {
+    kv_fork_kernel<<<1, PG_THREADS, ((size_t)n + 1) * sizeof(int), st>>>(table, n_rows, max_pages, ref, n_pages, pshift,
+                                                                         lens, parent, child, n, src, dst, info);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    kv_fork_rows_kernel<<<(unsigned)n, 128, 0, st>>>(table, max_pages, ref, n_pages, pshift, lens, parent, child, dst, info,
+                                                     status);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_release(int32_t* table, int n_rows, int max_pages, int32_t* ref, int n_pages, int32_t* lens,
+                              const int32_t* rows, int n, unsigned* status, cudaStream_t st) {
+    kv_release_kernel<<<(unsigned)n, 128, 0, st>>>(table, n_rows, max_pages, ref, n_pages, lens, rows, status);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_compact(int32_t* table, int n_rows, int max_pages, int32_t* ref, int n_pages, int32_t* map,
+                              int32_t* src, int32_t* dst, int32_t* info, unsigned* status, cudaStream_t st) {
+    kv_compact_kernel<<<1, PG_THREADS, 0, st>>>(ref, n_pages, map, src, dst, info);
+    cudaError_t e = cudaGetLastError();
+    const int64_t n = (int64_t)n_rows * max_pages;
+    if (e != cudaSuccess || n == 0) return e;
+    const int64_t blocks = (n + 255) / 256;
+    kv_remap_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, st>>>(table, n, map, n_pages, status);
+    return cudaGetLastError();
+}
+
+}  // namespace lq

@@ -311,6 +311,145 @@ int lq_moe_ffn_static(const float* router, int n_experts, int topk, int fmt, con
                       const float* X, float* Y, int ntok, int32_t* topk_idx, float* topk_w,
                       lq_stream_t stream);
 
+/* ---------------------------------------------------------------- positions, KV cache and attention
+ * The operators of a decode or prefill step between the QKV and the O
+ * projection: rotary positions, a paged KV cache held in 8 bits, attention
+ * over it and the bookkeeping of its pages.  q, k, v, outputs: fp32, a row
+ * per token; ld_* = floats between rows (>= heads * head_dim), heads
+ * adjacent.  No call allocates or synchronises; a captured graph may hold
+ * any of them.
+ *
+ * Steps.  A step adds tokens to nseq sequences.  cu: [nseq + 1] int32, the
+ * first new token row of each sequence, cu[0] = 0, cu[nseq] = ntok,
+ * ascending (NULL: one new token per sequence, ntok == nseq).  start:
+ * [nseq] int32, tokens of each sequence before the step: new token i of
+ * sequence s stands at position start[s] + i.  A negative position is
+ * padding (an idle slot of a captured graph, a left-padded prompt): it is
+ * not stored and its attention output is zero.  table: [rows][max_pages]
+ * int32, the page of positions [j * page, (j + 1) * page) of row (sequence)
+ * s at [s][j], -1 where there is none.  All of these are device memory,
+ * read by the kernels only.  A position past the table, a page index
+ * outside the pool or a row outside the table is not accessed: the token or
+ * key is left out and LQ_STATUS_BADARG is set in the device status word
+ * (lq_device_status). */
+#define LQ_STATUS_TIMEOUT 1u
+#define LQ_STATUS_BADARG 2u
+
+/* lq_kv8 -- one layer's cache: int8 codes in pages of `page` tokens, one
+ * fp32 scale per page and kv head.  Key of slot i of a page, dim d:
+ * k[page][head][i][d] * k_scale[page][head]; value: v[page][head][d][i] *
+ * v_scale[page][head] (a head's tokens adjacent: the attention reads them
+ * as such).  page: 16, 32, 64, 128 or 256; head_dim: 64, 128 or 256.
+ * k, v: 16-byte aligned.  The struct itself is host memory, read during the
+ * call. */
+typedef struct {
+    void* k;              /* int8 [n_pages][n_kv][page][head_dim] */
+    void* v;              /* int8 [n_pages][n_kv][head_dim][page] */
+    float* k_scale;       /* [n_pages][n_kv] */
+    float* v_scale;       /* [n_pages][n_kv] */
+    int64_t n_pages;
+    int32_t n_kv, page, head_dim;
+} lq_kv8;
+
+/* lq_rope -- rotary positions of the q and k rows of ntok tokens.  Pair i of
+ * a head (0 <= i < rot_dim / 2; rot_dim even, <= head_dim) is rotated by
+ * pos[axis[i]][t] * freq[i] radians: (a, b) -> (a cos - b sin, b cos + a sin).
+ * pairing: LQ_ROPE_HALF pairs elements i and i + rot_dim / 2, LQ_ROPE_ADJACENT
+ * 2i and 2i + 1.  Elements from rot_dim on are copied.  pos: [n_axes][ntok]
+ * int32 (one axis for text; time, height, width ... for images and video);
+ * axis: [rot_dim / 2] uint8, each < n_axes (NULL: axis 0); freq: [rot_dim / 2]
+ * fp64, radians per position.  The angle is reduced in fp64, so positions of
+ * any size keep fp32 accuracy.  q_out / k_out may equal q / k (with the same
+ * ld); k may be NULL with n_k 0. */
+enum { LQ_ROPE_HALF = 1, LQ_ROPE_ADJACENT = 2 };
+int lq_rope(const float* q, int n_q, int64_t ld_q, float* q_out, int64_t ld_qo, const float* k, int n_k,
+            int64_t ld_k, float* k_out, int64_t ld_ko, int head_dim, int rot_dim, int pairing, const int32_t* pos,
+            int n_axes, const uint8_t* axis, const double* freq, int ntok, lq_stream_t stream);
+
+/* lq_kv8_append -- stores the step's new K and V rows ([ntok][n_kv *
+ * head_dim]) in the cache.  For each page and head that gets new tokens:
+ *   s = max(s_old, amax / 127) (amax over the new values; s_old = 0 if the
+ *       page's first slot is among them), codes = x / s rounded to nearest
+ *       (ties to even; exactly), clamped to [-127, 127]; s = 0: codes 0;
+ *   if s > s_old, the page's earlier codes c become c * s_old (rounded to
+ *       fp32) / s rounded likewise.
+ * A NaN or infinite value makes the scale of its page and head NaN (its new
+ * codes 0): attention over that page gives NaN instead of wrong numbers.
+ * The pages written must belong to one sequence each (lq_kv_fork gives a
+ * child its own last page).  The table must already hold them
+ * (lq_kv_reserve). */
+int lq_kv8_append(const lq_kv8* cache, const int32_t* table, int max_pages, const int32_t* start, const int32_t* cu,
+                  int nseq, const float* k, int64_t ld_k, const float* v, int64_t ld_v, int ntok,
+                  lq_stream_t stream);
+
+/* lq_kv8_attn -- attention of the step's query rows over the cache (after
+ * lq_kv8_append of the same step).  n_q a multiple of n_kv; query head h
+ * reads kv head h / (n_q / n_kv).  For the query at position p and the key
+ * at j < start[s] + (new tokens of s):
+ *   t = scale * q.k;  softcap > 0: t = softcap * tanh(t / softcap);
+ *   slopes (optional, [n_q]): t -= slopes[h] * |p - j|;
+ *   visible if j <= p and (window == 0 or p - j < window), or j < prefix[s]
+ *   (optional, [nseq] int32: leading tokens that every query sees, also
+ *   those before them: an image prefix, or kept first tokens of a window);
+ *   out = sum_j softmax(t)_j v_j over the visible keys; zeros if there are
+ *   none.  Sequences never see each other (the document mask of a packed
+ *   batch).  fp32 in and out at fp32 accuracy: the tensor cores get q and
+ *   the softmax weights in two fp16 pieces each.  The result does not depend
+ *   on the stream or on timing.  workspace:
+ *   lq_kv8_attn_workspace_bytes(n_q, n_kv, head_dim, nseq, ntok) bytes, 256-byte
+ *   aligned, scratch of this call only (invalid sizes give 0). */
+size_t lq_kv8_attn_workspace_bytes(int n_q, int n_kv, int head_dim, int nseq, int ntok);
+int lq_kv8_attn(const lq_kv8* cache, const int32_t* table, int max_pages, const int32_t* start, const int32_t* cu,
+                int nseq, const float* q, int n_q, int64_t ld_q, int ntok, float scale, float softcap, int window,
+                const int32_t* prefix, const float* slopes, float* out, int64_t ld_out, void* workspace,
+                size_t ws_bytes, lq_stream_t stream);
+
+/* Pages.  ref: [n_pages] int32, the rows that hold each page (0 = free; all
+ * zero at first).  New pages are the free ones of lowest index, in ascending
+ * order.  info: 2 int32 written by the call: info[0] as stated, info[1] = 1
+ * if an argument on the device was out of range (nothing was changed then).
+ * A call that lacks pages changes nothing and says in info[0] how many are
+ * missing.
+ *
+ * lq_kv_reserve -- pages for the step's new tokens: every position from
+ * max(start[s], 0) to the step's end gets a page where row s has none (-1).
+ * info[0] = pages missing (0: done). */
+int lq_kv_reserve(int32_t* table, int max_pages, int32_t* ref, int n_pages, int page, const int32_t* start,
+                  const int32_t* cu, int nseq, int32_t* info, lq_stream_t stream);
+
+/* lq_kv_fork -- row child[i] becomes a copy of row parent[i] (i < n): it
+ * shares the full pages of the lens[parent] tokens (their ref counts grow)
+ * and, if the last page is partly filled, gets a new one: src[i] -> dst[i]
+ * is the copy to make in every layer (lq_kv8_copy_pages), -1 if none.
+ * lens[child] = lens[parent].  Children hold no pages before the call
+ * (lq_kv_release), are distinct and are no parents in it; one parent may have
+ * several.  n <= 4096.  info[0] = pages missing (src, dst = -1 then). */
+int lq_kv_fork(int32_t* table, int n_rows, int max_pages, int32_t* ref, int n_pages, int page, int32_t* lens,
+               const int32_t* parent, const int32_t* child, int n, int32_t* src, int32_t* dst, int32_t* info,
+               lq_stream_t stream);
+
+/* lq_kv_release -- rows[i] (i < n) give back their pages: each entry's ref
+ * count falls by one, the entries become -1 and lens[row] = 0 (lens may be
+ * NULL).  Releasing an empty row, or one row twice, changes nothing more. */
+int lq_kv_release(int32_t* table, int n_rows, int max_pages, int32_t* ref, int n_pages, int32_t* lens,
+                  const int32_t* rows, int n, lq_stream_t stream);
+
+/* lq_kv_compact -- closes the pool up: with u pages in use, the used pages
+ * of index >= u move, in ascending order, to the free ones below u, in
+ * ascending order.  table and ref are rewritten; map: [n_pages] int32, the
+ * new index of each old page (-1: free); src, dst: [n_pages / 2] int32, the
+ * copies to make in every layer (-1 past the last); info[0] = their number. */
+int lq_kv_compact(int32_t* table, int n_rows, int max_pages, int32_t* ref, int n_pages, int32_t* map, int32_t* src,
+                  int32_t* dst, int32_t* info, lq_stream_t stream);
+
+/* lq_kv8_copy_pages -- copies the codes and scales of page src[i] to page
+ * dst[i] for i < n in n_layers caches of one shape (layers: host array of
+ * pointers to lq_kv8).  Entries with src or dst < 0 are skipped; i >= count[0]
+ * too if count (device int32) is given.  The dst pages are distinct and none
+ * is a src. */
+int lq_kv8_copy_pages(const lq_kv8* const* layers, int n_layers, const int32_t* src, const int32_t* dst, int n,
+                      const int32_t* count, lq_stream_t stream);
+
 /* lq_device_status -- waits for all work on the current device (every
  * stream: the status word is one per device, shared by every launch of the
  * library, so a bit set by a launch on another stream is reported here
