@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(APP_THREADS) kv8_append_kernel(const KvView C,
     __syncthreads();
     for (int i = 0; i < APP_THREADS / 32; ++i) m = max(m, red[i]);
     const float was = s0 > 0 ? *scale : 0.f;
-    const float mine = m < 0x7F800000u ? __uint_as_float(m) / 127.f : __uint_as_float(0x7FC00000u);
+    const float mine = m < 0x7F800000u ? __uint_as_float(m) * (1.f / 127.f) : __uint_as_float(0x7FC00000u);
     const float now = kv_absbits(was) >= kv_absbits(mine) ? was : mine;  // NaN stays
     const bool good = kv_absbits(now) < 0x7F800000u && now > 0.f;
     const bool again = s0 > 0 && good && now > was;                      // earlier codes get the new scale

@@ -340,7 +340,7 @@ int lq_moe_ffn_static(const float* router, int n_experts, int topk, int fmt, con
  * k[page][head][i][d] * k_scale[page][head]; value: v[page][head][d][i] *
  * v_scale[page][head] (a head's tokens adjacent: the attention reads them
  * as such).  page: 16, 32, 64, 128 or 256; head_dim: 64, 128 or 256.
- * k, v: 16-byte aligned.  The struct itself is host memory, read during the
+ * k, v: 16-byte aligned; scales >= 0.  The struct itself is host memory, read during the
  * call. */
 typedef struct {
     void* k;              /* int8 [n_pages][n_kv][page][head_dim] */
@@ -368,9 +368,10 @@ int lq_rope(const float* q, int n_q, int64_t ld_q, float* q_out, int64_t ld_qo, 
 
 /* lq_kv8_append -- stores the step's new K and V rows ([ntok][n_kv *
  * head_dim]) in the cache.  For each page and head that gets new tokens:
- *   s = max(s_old, amax / 127) (amax over the new values; s_old = 0 if the
- *       page's first slot is among them), codes = x / s rounded to nearest
- *       (ties to even; exactly), clamped to [-127, 127]; s = 0: codes 0;
+ *   s = max(s_old, amax * (1 / 127 in fp32)) (amax over the new values;
+ *       s_old = 0 if the page's first slot is among them), codes = x / s
+ *       rounded to nearest (ties to even; exactly), clamped to [-127, 127];
+ *       s = 0: codes 0;
  *   if s > s_old, the page's earlier codes c become c * s_old (rounded to
  *       fp32) / s rounded likewise.
  * A NaN or infinite value makes the scale of its page and head NaN (its new

@@ -73,7 +73,7 @@ class Cache:
         for h in range(self.n_kv):
             for codes, scales, x in ((self.k[page, h], self.ks, k[:, h]), (self.v[page, h].T, self.vs, v[:, h])):
                 was = scales[page, h] if slot > 0 else np.float32(0)
-                mine = np.abs(x).max() / np.float32(127) if np.isfinite(x).all() else np.float32(np.nan)
+                mine = np.abs(x).max() * (np.float32(1) / np.float32(127)) if np.isfinite(x).all() else np.float32(np.nan)
                 now = was if np.isnan(was) or was >= mine else mine
                 good = np.isfinite(now) and now > 0
                 if good and slot > 0 and now > was:

@@ -131,7 +131,7 @@ def test_append_statement_by_hand():
     x[0, 0], x[1, 1], x[2, 2] = 1.27, 2.54, 0.635
     for i in range(3):
         c.append(table, [i], [0, 1], x[i:i + 1], -x[i:i + 1])
-    assert c.ks[0, 0] == np.float32(2.54) / np.float32(127)
+    assert c.ks[0, 0] == np.float32(2.54) * (np.float32(1) / np.float32(127))
     assert c.k[0, 0, 0, 0] == 64 and c.k[0, 0, 1, 1] == 127 and c.k[0, 0, 2, 2] == 32     # 63.5 and 31.75: to even, up
     assert c.v[0, 0, 0, 0] == -64 and c.v[0, 0, 1, 1] == -127
 
