@@ -1,0 +1,113 @@
+// lq_kv8_attn.cuh -- what the attention kernels over the 8-bit cache share:
+// the visibility rule of a sequence, the score epilogue and the fp16 pieces.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "lq_internal.h"
+#include "lq_kv.cuh"
+
+namespace lq {
+
+constexpr float ATT_LOG2E = 1.4426950408889634f;
+// Softmax weights are formed as 2^(u - max + ATT_SHIFT): at most 2^13, so the
+// fp16 hi piece keeps 11 bits and the lo piece the next 11 down to 2^-24,
+// 2^-37 of the largest weight.  Numerator and denominator carry the same
+// factor, so it cancels.
+constexpr float ATT_SHIFT = 13.f;
+
+__device__ __forceinline__ float att_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// tanh to fp32 rounding: an odd polynomial (least-squares fit of tanh(x) / x
+// in x^2, relative error 3e-9) up to 0.6, where 1 - 2 / (e^2x + 1) would
+// cancel, and that form beyond (its error is then below 2^-23 of the value).
+__device__ __forceinline__ float att_tanh(float x) {
+    const float z = x * x;
+    float p = fmaf(z, -0.005852157715708017f, 0.020753618329763412f);
+    p = fmaf(p, z, -0.05376870185136795f);
+    p = fmaf(p, z, 0.13331688940525055f);
+    p = fmaf(p, z, -0.3333328366279602f);
+    const float small = fmaf(x * z, p, x);
+    const float big = 1.f - __fdividef(2.f, att_ex2(fminf(fabsf(x), 20.f) * (2.f * ATT_LOG2E)) + 1.f);
+    return fabsf(x) <= 0.6f || x != x ? small : copysignf(big, x);
+}
+
+// Two fp32 values as fp16 pieces: hi + lo = (x, y) to 2^-22 relative.
+__device__ __forceinline__ void att_split(float x, float y, uint32_t& hi, uint32_t& lo) {
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+// Four int8 codes (bytes of w) as exact fp16 pairs (0, 1) and (2, 3): the
+// byte with its sign bit flipped is code + 128, which as the low byte of an
+// fp16 0x64xx reads 1024 + 128 + code.
+__device__ __forceinline__ void att_codes(uint32_t w, uint32_t& a, uint32_t& b) {
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));     // 1152
+    const uint32_t x = prmt(u, 0x64646464u, 0x4140u), y = prmt(u, 0x64646464u, 0x4342u);
+    const __half2 p = __hsub2(*reinterpret_cast<const __half2*>(&x), off);
+    const __half2 q = __hsub2(*reinterpret_cast<const __half2*>(&y), off);
+    a = *reinterpret_cast<const uint32_t*>(&p);
+    b = *reinterpret_cast<const uint32_t*>(&q);
+}
+
+// What a sequence's query rows can see: keys below len; all of them [0, pre)
+// and, with a window, nothing else below the window of the first row.
+struct AttSeq {
+    int32_t s, row0, n;      // sequence, first query row, query rows
+    int64_t start;           // position of the first query row
+    int32_t len, pre;        // keys; leading keys that every row sees
+    int32_t lo;              // first key that the earliest row's window holds
+};
+__device__ __forceinline__ AttSeq att_seq(const AttnParams& P, int s) {
+    AttSeq q;
+    q.s = s;
+    q.row0 = kv_cu(P.s, s);
+    q.n = kv_cu(P.s, s + 1) - q.row0;
+    if (q.n < 0 || q.row0 < 0 || q.row0 + q.n > P.s.ntok) q.n = 0;       // not a step: nothing of it is touched
+    q.start = __ldg(P.s.start + s);
+    const int64_t end = q.start + q.n, held = (int64_t)P.s.max_pages << P.c.pshift;
+    q.len = (int)max((int64_t)0, min(min(end, held), (int64_t)INT32_MAX - 1024));
+    q.pre = P.prefix ? min(max(__ldg(P.prefix + s), 0), q.len) : 0;
+    const int64_t p0 = max(q.start, (int64_t)0);
+    q.lo = P.window ? (int)min(max(p0 - P.window + 1, (int64_t)0), (int64_t)q.len) : 0;
+    return q;
+}
+
+// Whether the query at position p sees key j (j < len).
+__device__ __forceinline__ bool att_sees(const AttnParams& P, const AttSeq& q, int p, int j) {
+    return j < q.len && p >= 0 && (j < q.pre || (j <= p && (P.window == 0 || p - j < P.window)));
+}
+
+// The page of a sequence's position, -1 if there is none.
+__device__ __forceinline__ int att_page(const AttnParams& P, int s, int pos) {
+    const int pj = pos >> P.c.pshift;
+    const int pg = pj < P.s.max_pages ? __ldg(P.s.table + (int64_t)s * P.s.max_pages + pj) : -1;
+    return pg >= 0 && pg < P.c.n_pages ? pg : -1;
+}
+
+// Power of two near a value scale, the reference of a row's weights: the
+// softmax weights times the value scales are formed in one exponent, 2^(t
+// log2 e + log2(vs / 2^e0) - max), so that no page's scale can overflow the
+// fp16 pieces and the log stays near 0 (and exact to 2^-24) for scales near
+// this one.  Unusable scales (0, NaN) give 0.
+__device__ __forceinline__ int att_e0(float vs) {
+    const int e = (int)((__float_as_uint(vs) >> 23) & 0xFFu);
+    return vs > 0.f && e < 255 ? min(max(e - 127, -100), 100) : 0;
+}
+// A page's value scale over the reference (x = vs / 2^e0) as the weights use
+// it: 1 with `zero` set where it is 0 or below 2^-90 (the keys count in the
+// sum, their values are 0), NaN where it is NaN or above 2^90.
+__device__ __forceinline__ float att_rel(float x, bool& zero) {
+    zero = x < 0x1p-90f;
+    return zero ? 1.f : x > 0x1p90f ? __uint_as_float(0x7FC00000u) : x;
+}
+__device__ __forceinline__ float att_pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+}  // namespace lq
