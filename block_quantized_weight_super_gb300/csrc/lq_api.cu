@@ -569,6 +569,31 @@ int tensor_map(CUtensorMap* out, const void* base, int64_t rows, int64_t rowbyte
     return LQ_OK;
 }
 
+}  // namespace
+
+// A tensor map over bytes [d2][d1][d0] with boxes of [1][b1][b0] (lq_internal.h).
+int api_byte_map(CUtensorMap* out, const void* base, int64_t d0, int64_t d1, int64_t d2, int b0, int b1) {
+    std::lock_guard<std::mutex> lk(g_map_mu);
+    if (!g_encode) {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+        if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !fn)
+            return fail(LQ_ECUDA, "cuTensorMapEncodeTiled entry point unavailable");
+        g_encode = reinterpret_cast<EncodeTiledFn>(fn);
+    }
+    const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
+    const cuuint64_t strides[2] = {(cuuint64_t)d0, (cuuint64_t)(d0 * d1)};
+    const cuuint32_t box[3] = {(cuuint32_t)b0, (cuuint32_t)b1, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = g_encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? LQ_OK : fail(LQ_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+}
+
+namespace {
+
 
 // ---------------------------------------------------------------- batch-1 tensor-core path
 // Segments of one x row (no device counts or gathers), Q4_K alone or Q4_K

@@ -290,5 +290,7 @@ int api_fail(int code, const char* fmt, ...);
 int api_cuda_fail(cudaError_t e, const char* what);
 void api_clear();
 int api_device(ApiDevice* out);          // an lq_status
+// a tensor map over bytes [d2][d1][d0], boxes of [1][b1][b0] (an lq_status)
+int api_byte_map(CUtensorMap* out, const void* base, int64_t d0, int64_t d1, int64_t d2, int b0, int b1);
 
 }  // namespace lq

@@ -17,18 +17,18 @@
 // 16-byte piece.  Four codes become two fp16 pairs in five instructions.
 //
 // Split.  (sequence, kv head, row tile, chunk) are numbered in one line and
-// dealt to the warps of one CTA per SM in equal shares, whatever the
-// lengths; warps never meet.  A warp keeps a running maximum, sum and O for
-// its stretch of a tile; a tile that spans several warps leaves one partial
-// result per warp and kv8_combine_kernel joins them in order.  The share
-// boundaries depend on the lengths and the SM count only, so results are
-// reproducible.
+// dealt to the consumer warps of one CTA per SM in equal shares, whatever the
+// lengths; they never meet.  A warp keeps a running maximum, sum and O for its
+// stretch of a tile; a tile that spans several warps leaves one partial
+// result per warp and kv8_combine_kernel joins them in order.  The shares
+// depend on the lengths and the SM count only, so results are reproducible.
 //
-// Loads.  Each warp streams its chunks through its own ring of half-chunks
-// (K, then V) with 16-byte cp.async, two or more halves in flight: 8 warps x
-// 16 KB cover 6.8 TB/s x 1 us = 45 KB per SM with room.  Shared memory is
-// swizzled so that both the copies and the fragment reads are free of bank
-// conflicts.
+// Loads.  One warp more per CTA is the producer: its lane i walks consumer
+// i's share ahead of it, reads the page table and copies K, then V of each
+// chunk into the consumer's ring of half-chunks (bulk copies; a tensor copy
+// where a chunk is a slice of a page's V rows), with full / empty barriers.
+// That keeps addresses, page lookups and the copies' registers out of the
+// consumers, whose instruction issue is what limits them.
 #include "lq_kv8_attn.cuh"
 
 namespace lq {
@@ -36,29 +36,37 @@ namespace {
 
 template <int D>
 struct Dc {
-    static constexpr int T = D == 256 ? 32 : 64;             // keys of a chunk
+    static constexpr int T = D == 64 ? 64 : 32;              // keys of a chunk
     static constexpr int TQ = T / 4;                         // keys of a thread of a quad
-    static constexpr int NW = D == 256 ? 6 : 8;              // warps of a CTA
-    static constexpr int NSLOT = D == 64 ? 6 : 3;            // half-chunks of a warp's ring
+    static constexpr int NC = D == 64 ? 15 : D == 128 ? 11 : 7;    // consumer warps (with the producer 4, 3 or 2 per scheduler)
+    static constexpr int NT = (NC + 1) * 32;
+    static constexpr int NSLOT = D == 256 ? 2 : 3;   // half-chunks of a consumer's ring
     static constexpr int HB = T * D;                         // bytes of a half-chunk
-    static constexpr bool QS = D == 256;                     // q fragments in shared memory (registers are full)
-    static constexpr int QB = QS ? D * 32 : 0;
+    static constexpr int HBP = HB + 128;                     // with the padding between pages of V
+    static constexpr int QB = D * 32;                        // q fragments
     static constexpr int NMETA = 4;                          // chunks whose scales are held
-    static constexpr int WB = NSLOT * HB + QB + NMETA * 64;  // shared memory of a warp
-    static constexpr int SMEM = NW * WB;
-    static constexpr int SUB = D / 16;                       // 16-byte pieces of a key
+    static constexpr int WB = NSLOT * HBP + QB + NMETA * 64; // shared memory of a consumer (a multiple of 128)
+    static constexpr int SMEM = NC * WB;
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Arrives on the barrier (one of its expected arrivals) once this thread's
+// cp.async so far have landed.
+__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
 }
 __device__ __forceinline__ uint4 ld_s128(uint32_t a) {
     uint4 v;
@@ -134,15 +142,20 @@ __host__ __device__ inline size_t base_bytes(int nseq) { return ((size_t)(nseq +
 __device__ __forceinline__ int owner(int64_t u, int64_t U, int W) { return (int)(((u + 1) * W - 1) / U); }
 
 template <int D, bool EXTRA>
-__global__ void __launch_bounds__(Dc<D>::NW * 32, 1) kv8_decode_kernel(const AttnParams P) {
+__global__ void __launch_bounds__(Dc<D>::NT, 1) kv8_decode_kernel(const AttnParams P, const __grid_constant__ CUtensorMap vmap) {
     using F = Dc<D>;
-    constexpr int T = F::T, TQ = F::TQ, NS = TQ / 4, NT = F::NW * 32;
+    constexpr int T = F::T, TQ = F::TQ, NS = TQ / 4, NT = F::NT, NC = F::NC, NSLOT = F::NSLOT;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t tb[NT + 1];
-    __shared__ int64_t wsum[F::NW];
+    __shared__ int64_t tb[NT];
+    __shared__ int64_t wsum[NC + 1];
+    __shared__ uint64_t full[NC][NSLOT], empty[NC][NSLOT];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     pdl_launch_dependents();
-    pdl_wait();
+    if (tid < NC * NSLOT) {
+        mbar_init(&full[0][0] + tid, 2);                  // the producer's two arrivals
+        mbar_init(&empty[0][0] + tid, 1);
+        fence_mbar_init();
+    }
 
     // ---- the line: thread i sums the units of its sequences
     const int per = (P.s.nseq + NT - 1) / NT;
@@ -157,7 +170,7 @@ __global__ void __launch_bounds__(Dc<D>::NW * 32, 1) kv8_decode_kernel(const Att
     if (lane == 31) wsum[warp] = inc;
     __syncthreads();
     int64_t before = 0, U = 0;
-    for (int i = 0; i < F::NW; ++i) {
+    for (int i = 0; i < NC + 1; ++i) {
         if (i < warp) before += wsum[i];
         U += wsum[i];
     }
@@ -173,14 +186,17 @@ __global__ void __launch_bounds__(Dc<D>::NW * 32, 1) kv8_decode_kernel(const Att
     }
     __syncthreads();
 
-    // warps in use (none without a unit) and this one: few units go to different SMs
-    const int W = (int)min((int64_t)gridDim.x * F::NW, U), w = warp * gridDim.x + blockIdx.x;
-    if (w >= W) return;                                   // warps never meet again
-    const int64_t u0 = U * w / W, u1 = U * (w + 1) / W;
-    const int nu = (int)(u1 - u0);
-    Cur cc;                                               // what is computed
-    {
-        int i = kv_find(NT, u0, [&](int x) { return tb[x]; });
+    // consumers in use (none without a unit) and the one this thread works
+    // for; few units go to different SMs
+    const bool producer = warp == NC;
+    const int ci = producer ? min(lane, NC - 1) : warp;
+    const int W = (int)min((int64_t)gridDim.x * NC, U), w = ci * gridDim.x + blockIdx.x;
+    if (w >= W && !producer) return;
+    const int64_t u0 = w < W ? U * w / W : 0;
+    const int nu = w < W && (!producer || lane < NC) ? (int)(U * (w + 1) / W - u0) : 0;
+    Cur cc{};                                             // the unit at hand
+    if (nu > 0) {
+        const int i = kv_find(NT, u0, [&](int x) { return tb[x]; });
         int64_t b = tb[i];
         int s = i * per;
         for (;; ++s) {
@@ -194,70 +210,112 @@ __global__ void __launch_bounds__(Dc<D>::NW * 32, 1) kv8_decode_kernel(const Att
         cc.tile = (int)(item % cc.d.tiles);
         cc.hk = (int)(item / cc.d.tiles);
     }
-    Cur ci = cc;                                          // what is loaded
-
-    const uint32_t wbase = smem_u32(smem) + warp * F::WB, qbase = wbase + F::NSLOT * F::HB, mbase = qbase + F::QB;
+    const uint32_t wbase = smem_u32(smem) + ci * F::WB, qbase = wbase + NSLOT * F::HBP, mbase = qbase + F::QB;
     const int pshift = P.c.pshift, Pg = 1 << pshift;
-    const int64_t blk = (int64_t)D << pshift;             // bytes of a page's head
-    int pg = -1;                                          // page of this thread's keys in the chunk to load
-    auto load_page = [&]() {
-        const int pos = cur_chunk(ci) * T + TQ * t;
-        pg = pos < ci.d.q.len ? att_page(P, ci.d.q.s, pos) : -1;
-    };
-    load_page();
-    int64_t gb = -1;                                      // byte offset of that page and head, -1: none
-    int iu = 0;                                           // units whose K was loaded
 
-    // half-chunk h: K (even) or V (odd) of unit h / 2
-    auto issue = [&](int h) {
-        if (h < 2 * nu) {
-            const uint32_t slot = wbase + (h % F::NSLOT) * F::HB;
-            const int tok = cur_chunk(ci) * T + TQ * t;
-            if ((h & 1) == 0) {
-                gb = pg < 0 ? -1 : ((int64_t)pg * P.c.n_kv + ci.hk) * blk;
-                const int64_t kb = gb < 0 ? -1 : gb + (int64_t)(tok & (Pg - 1)) * D;
+    if (producer) {
+        const int pw = min(Pg, T), npg = T / pw;           // keys of a chunk per page, pages of a chunk
+        const int64_t blk = (int64_t)D << pshift;         // bytes of a page's head
+        const uint32_t pb = (uint32_t)pw * D, pad = npg > 1 ? 128u / npg : 0u;
+        int pg[4], nx[4];                                 // pages of this unit, of the next one
+        auto pages = [&](const Cur& k, int (&out)[4]) {
 #pragma unroll
-                for (int i = 0; i < F::HB / 512; ++i) {
-                    const int idx = i * 32 + lane, r = idx / F::SUB, u = idx % F::SUB;
-                    const int64_t b = __shfl_sync(0xFFFFFFFFu, kb, r / TQ);
-                    const int sw = D >= 128 ? (r & 1) << 2 : 0;
-                    if (b >= 0) cp16(slot + r * D + ((u ^ sw) << 4), P.c.k + b + (r % TQ) * D + u * 16);
-                }
-                // scales: threads 0-3 K's, 4-7 V's of key groups 0-3
-                if (lane < 8) {
-                    const uint32_t m = mbase + (iu % F::NMETA) * 64 + (lane >> 2) * 16 + t * 4;
-                    const int64_t ph = gb < 0 ? 0 : (int64_t)pg * P.c.n_kv + ci.hk;
-                    if (gb >= 0) cp4(m, (lane < 4 ? P.c.ks : P.c.vs) + ph);
-                    else st_sf(m, 0.f);
-                    if (lane < 4) st_sf(m + 32, gb < 0 ? 0.f : 1.f);
-                }
-            } else {
-                // V: `upd` 16-byte pieces per dim in each of the chunk's pages
-                const int lu = min(pshift - 4, T == 64 ? 2 : 1);
-                const int64_t vb = gb < 0 ? -1 : gb + ((tok & (Pg - 1)) & ~15);
+            for (int i = 0; i < 4; ++i) {
+                const int pos = cur_chunk(k) * T + i * pw;
+                out[i] = i < npg && pos < k.d.q.len ? att_page(P, k.d.q.s, pos) : -1;
+            }
+        };
+        Cur cn = cc;
+        if (nu > 0) {
+            pages(cc, pg);
+            if (nu > 1) {
+                cur_next<T>(P, cn);
+                pages(cn, nx);
+            }
+        }
+        int h = 0;
+        bool stop = nu == 0;
+        uint64_t idle0 = 0;                               // since when this lane has waited
+        while (__any_sync(0xFFFFFFFFu, !stop)) {
+            const int slot = h % NSLOT;
+            const bool go = !stop && (h < NSLOT || mbar_try_wait(&empty[ci][slot], (uint32_t)((h / NSLOT - 1) & 1)));
+            if (go) {
+                idle0 = 0;
+                uint64_t* bar = &full[ci][slot];
+                const uint32_t dst = wbase + slot * F::HBP;
+                int n = 0;
 #pragma unroll
-                for (int i = 0; i < F::HB / 512; ++i) {
-                    const int idx = i * 32 + lane;
-                    const int pi = idx / D >> lu, rem = idx - ((pi << lu) * D), d = rem >> lu, u = rem & ((1 << lu) - 1);
-                    const int unit = (pi << lu) + u;                         // 16-byte piece of the chunk's row of dim d
-                    const int64_t b = __shfl_sync(0xFFFFFFFFu, vb, T == 64 ? (pi << lu) : (pi << lu) * 2);
-                    const int sw = T == 64 ? (d >> 1) & 3 : (d >> 2) & 1;
-                    if (b >= 0) cp16(slot + d * T + ((unit ^ sw) << 4), P.c.v + b + ((int64_t)d << pshift) + u * 16);
+                for (int i = 0; i < 4; ++i) n += i < npg && pg[i] >= 0;
+                const int off = cur_chunk(cc) * T & (Pg - 1);               // the chunk's place in its page (npg = 1)
+                if ((h & 1) == 0) {
+                    const uint32_t m = mbase + (h / 2 % F::NMETA) * 64;
+#pragma unroll
+                    for (int i = 0; i < T / 16; ++i) {
+                        const int p = pg[npg == 1 ? 0 : i * 16 / pw];
+                        st_sf(m + 32 + 4 * i, p < 0 ? 0.f : 1.f);
+                        if (p < 0) {
+                            st_sf(m + 4 * i, 0.f);
+                            st_sf(m + 16 + 4 * i, 0.f);
+                        }
+                    }
+                    if (n > 0) mbar_arrive_expect_tx(bar, n * pb);
+                    else mbar_arrive(bar);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < npg && pg[i] >= 0)
+                            bulk_copy(dst + i * pb, P.c.k + ((int64_t)pg[i] * P.c.n_kv + cc.hk) * blk + (int64_t)off * D, pb, bar);
+#pragma unroll
+                    for (int i = 0; i < T / 16; ++i) {
+                        const int p = pg[npg == 1 ? 0 : i * 16 / pw];
+                        if (p >= 0) {
+                            cp4(m + 4 * i, P.c.ks + (int64_t)p * P.c.n_kv + cc.hk);
+                            cp4(m + 16 + 4 * i, P.c.vs + (int64_t)p * P.c.n_kv + cc.hk);
+                        }
+                    }
+                    cp_arrive(bar);
+                } else {
+                    if (n > 0) mbar_arrive_expect_tx(bar, n * pb);
+                    else mbar_arrive(bar);
+                    mbar_arrive(bar);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < npg && pg[i] >= 0) {
+                            const int64_t ph = (int64_t)pg[i] * P.c.n_kv + cc.hk;
+                            if (pw == Pg) bulk_copy(dst + i * (pb + pad), P.c.v + ph * blk, pb, bar);
+                            else tma_load_3d(dst, &vmap, off, 0, (int)ph, bar);
+                        }
+                    // the next unit, whose pages are here, and the pages of the one behind it
+                    cc = cn;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) pg[i] = nx[i];
+                    if (h / 2 + 2 < nu) {
+                        cur_next<T>(P, cn);
+                        pages(cn, nx);
+                    }
                 }
-                if (++iu < nu) {
-                    cur_next<T>(P, ci);
-                    load_page();
+                stop = ++h == 2 * nu;
+            } else if (!stop) {
+                const uint64_t now = globaltimer_ns();
+                if (idle0 == 0) {
+                    idle0 = now;
+                } else if (now - idle0 > P.timeout_ns) {
+                    record_status(P.status, STATUS_TIMEOUT);
+                    stop = true;
                 }
             }
         }
-        cp_commit();
-    };
-    for (int h = 0; h < F::NSLOT - 1; ++h) issue(h);
+        // the last copies have landed before the CTA may exit
+        for (int k = max(0, h - NSLOT); k < h; ++k)
+            if (!mbar_wait_bounded(&full[ci][k % NSLOT], (uint32_t)((k / NSLOT) & 1), drain_bound(P.timeout_ns)))
+                record_status(P.status, STATUS_TIMEOUT);
+        return;
+    }
 
     const int grp = P.n_q / P.c.n_kv;
     float* part = reinterpret_cast<float*>(P.ws + base_bytes(P.s.nseq));
+    const int vw = min(Pg, T);                            // keys per row of V in shared memory
+    const uint32_t voff = (uint32_t)(TQ * t / vw) * ((uint32_t)vw * D + (vw < T ? 128u / (T / vw) : 0u)) + (TQ * t) % vw + g * vw;
     float o[D / 8][4];
-    uint32_t qf[F::QS ? 1 : D / 16][4];
     float m = -INFINITY, l = 0.f, qs = 0.f, slope = 0.f;
     int p = 0, e0 = 0;
     bool rowok = false, fresh = true, from_start = false;
@@ -277,27 +335,37 @@ __global__ void __launch_bounds__(Dc<D>::NW * 32, 1) kv8_decode_kernel(const Att
             head = cc.hk * grp + (rowok ? r % grp : 0);
             qrow = q.row0 + i;
             p = (int)min(max(q.start + i, (int64_t)-1), (int64_t)INT32_MAX - 1);
-            slope = P.slopes ? __ldg(P.slopes + head) : 0.f;
+            const float* x = P.q + qrow * P.ld_q + (int64_t)head * D + 16 * t;
             const int pe = att_page(P, q.s, cc.d.na > 0 ? 0 : min(cc.d.cb * T, q.len - 1));
-            e0 = pe >= 0 ? att_e0(__ldg(P.c.vs + (int64_t)pe * P.c.n_kv + cc.hk)) : 0;
-            is = att_pow2(-e0);
-            const float* x = P.q + qrow * P.ld_q + (int64_t)head * D;
             // the row's largest |q| and its power of two
             float mx = 0.f;
             float v[D / 64][16];
+            const bool vec = ((reinterpret_cast<uintptr_t>(P.q) | (P.ld_q * 4)) & 15) == 0;
 #pragma unroll
             for (int a = 0; a < D / 64; ++a)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    v[a][e] = rowok ? __ldg(x + 64 * a + 16 * t + e) : 0.f;
-                    mx = fmaxf(mx, fabsf(v[a][e]));
+                for (int e = 0; e < 16; e += 4) {
+                    float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+                    const float* y = x + 64 * a + e;
+                    if (rowok) z = vec ? __ldg(reinterpret_cast<const float4*>(y)) : make_float4(__ldg(y), __ldg(y + 1), __ldg(y + 2), __ldg(y + 3));
+                    v[a][e] = z.x;
+                    v[a][e + 1] = z.y;
+                    v[a][e + 2] = z.z;
+                    v[a][e + 3] = z.w;
                 }
+            slope = P.slopes ? __ldg(P.slopes + head) : 0.f;
+            e0 = pe >= 0 ? att_e0(__ldg(P.c.vs + (int64_t)pe * P.c.n_kv + cc.hk)) : 0;
+            is = att_pow2(-e0);
+#pragma unroll
+            for (int a = 0; a < D / 64; ++a)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) mx = fmaxf(mx, fabsf(v[a][e]));
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
             const int es = max(1, (int)((__float_as_uint(mx) >> 23) & 0xFFu) - 14);
             const float inv = __uint_as_float((uint32_t)(254 - es) << 23);
             qs = __uint_as_float((uint32_t)es << 23) * P.scale;
-            if (F::QS) __syncwarp();                      // every lane has read the last tile's fragments
+            __syncwarp();                                 // every lane has read the last tile's fragments
 #pragma unroll
             for (int a = 0; a < D / 64; ++a)
 #pragma unroll
@@ -305,14 +373,9 @@ __global__ void __launch_bounds__(Dc<D>::NW * 32, 1) kv8_decode_kernel(const Att
                     uint32_t f[4];
                     att_split(v[a][4 * k] * inv, v[a][4 * k + 1] * inv, f[0], f[1]);
                     att_split(v[a][4 * k + 2] * inv, v[a][4 * k + 3] * inv, f[2], f[3]);
-                    if (F::QS) {
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(qbase + ((4 * a + k) * 32 + lane) * 16),
-                                     "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3])
-                                     : "memory");
-                    } else {
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) qf[F::QS ? 0 : 4 * a + k][z] = f[z];
-                    }
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(qbase + ((4 * a + k) * 32 + lane) * 16),
+                                 "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3])
+                                 : "memory");             // (read back by this lane alone)
                 }
             m = -INFINITY;
             l = 0.f;
@@ -324,10 +387,11 @@ __global__ void __launch_bounds__(Dc<D>::NW * 32, 1) kv8_decode_kernel(const Att
 
         // ---- S = Q K^T
         const int hK = 2 * u;
-        cp_wait<F::NSLOT - 2>();
-        __syncwarp();
-        issue(hK + F::NSLOT - 1);
-        const uint32_t mt = mbase + (u % F::NMETA) * 64 + t * 4;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[ci][hK % NSLOT], (uint32_t)((hK / NSLOT) & 1), P.timeout_ns))) {
+            record_status(P.status, STATUS_TIMEOUT);
+            return;
+        }
+        const uint32_t mt = mbase + (u % F::NMETA) * 64 + (TQ * t / 16) * 4;
         const float ks = ld_sf(mt), vs = ld_sf(mt + 16);
         const bool held = ld_sf(mt + 32) != 0.f;
         float s[NS][2][4];
@@ -338,30 +402,23 @@ __global__ void __launch_bounds__(Dc<D>::NW * 32, 1) kv8_decode_kernel(const Att
 #pragma unroll
                 for (int z = 0; z < 4; ++z) s[x][j][z] = 0.f;
         {
-            const uint32_t slot = wbase + (hK % F::NSLOT) * F::HB;
+            const uint32_t kb = wbase + (hK % NSLOT) * F::HBP + (TQ * (g >> 1) + (g & 1)) * D + 16 * t;
 #pragma unroll
             for (int a = 0; a < D / 64; ++a) {
                 uint32_t qa[4][4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    if (F::QS) {
-                        const uint4 f = ld_s128(qbase + ((4 * a + k) * 32 + lane) * 16);
-                        qa[k][0] = f.x;
-                        qa[k][1] = f.y;
-                        qa[k][2] = f.z;
-                        qa[k][3] = f.w;
-                    } else {
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) qa[k][z] = qf[F::QS ? 0 : 4 * a + k][z];
-                    }
+                    const uint4 f = ld_s128(qbase + ((4 * a + k) * 32 + lane) * 16);
+                    qa[k][0] = f.x;
+                    qa[k][1] = f.y;
+                    qa[k][2] = f.z;
+                    qa[k][3] = f.w;
                 }
 #pragma unroll
                 for (int x = 0; x < NS; ++x)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const int r = TQ * (g >> 1) + 4 * x + 2 * j + (g & 1);
-                        const int sw = D >= 128 ? (g & 1) << 2 : 0;
-                        const uint4 kw = ld_s128(slot + r * D + (((4 * a + t) ^ sw) << 4));
+                        const uint4 kw = ld_s128(kb + (4 * x + 2 * j) * D + 64 * a);
                         const uint32_t wv[4] = {kw.x, kw.y, kw.z, kw.w};
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -372,13 +429,15 @@ __global__ void __launch_bounds__(Dc<D>::NW * 32, 1) kv8_decode_kernel(const Att
                     }
             }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[ci][hK % NSLOT]);
 
         // ---- weights
-        const int chunk = cur_chunk(cc), j0 = chunk * T, jt = j0 + TQ * t;
-        const bool full = held && j0 + T <= q.len &&
-                          (!rowok || (p >= 0 && (j0 + T <= q.pre ||
-                                                 (j0 + T - 1 <= p && (P.window == 0 || p - j0 < P.window)))));
-        const bool all_full = __all_sync(0xFFFFFFFFu, full);
+        const int j0 = cur_chunk(cc) * T, jt = j0 + TQ * t;
+        const bool whole = held && j0 + T <= q.len &&
+                           (!rowok || (p >= 0 && (j0 + T <= q.pre ||
+                                                  (j0 + T - 1 <= p && (P.window == 0 || p - j0 < P.window)))));
+        const bool all_whole = __all_sync(0xFFFFFFFFu, whole);
         bool vzero;
         const float rel = att_rel(vs * is, vzero), lv = log2f(rel);
         const float f = qs * ks * (EXTRA ? 1.f : ATT_LOG2E);
@@ -399,7 +458,7 @@ __global__ void __launch_bounds__(Dc<D>::NW * 32, 1) kv8_decode_kernel(const Att
                     } else {
                         v = fmaf(v, f, lv);
                     }
-                    if (!all_full && rowok) {
+                    if (!all_whole && rowok) {
                         const bool see = att_sees(P, q, p, jj);
                         if (see && !held) record_status(P.status, STATUS_BADARG);
                         if (!see || !held) v = -INFINITY;
@@ -437,25 +496,25 @@ __global__ void __launch_bounds__(Dc<D>::NW * 32, 1) kv8_decode_kernel(const Att
 
         // ---- O += W V
         const int hV = hK + 1;
-        cp_wait<F::NSLOT - 2>();
-        __syncwarp();
-        issue(hV + F::NSLOT - 1);
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[ci][hV % NSLOT], (uint32_t)((hV / NSLOT) & 1), P.timeout_ns))) {
+            record_status(P.status, STATUS_TIMEOUT);
+            return;
+        }
         {
-            const uint32_t slot = wbase + (hV % F::NSLOT) * F::HB;
+            const uint32_t vb = wbase + (hV % NSLOT) * F::HBP + voff;
 #pragma unroll
             for (int n = 0; n < D / 8; ++n) {
-                const int d = 8 * n + g;
                 uint32_t wv[4];
                 if (T == 64) {
-                    const uint4 vw = ld_s128(slot + d * T + ((t ^ ((d >> 1) & 3)) << 4));
-                    wv[0] = vw.x;
-                    wv[1] = vw.y;
-                    wv[2] = vw.z;
-                    wv[3] = vw.w;
+                    const uint4 z = ld_s128(vb + 8 * n * vw);
+                    wv[0] = z.x;
+                    wv[1] = z.y;
+                    wv[2] = z.z;
+                    wv[3] = z.w;
                 } else {
-                    const uint2 vw = ld_s64(slot + d * T + (((t >> 1) ^ ((d >> 2) & 1)) << 4) + (t & 1) * 8);
-                    wv[0] = vw.x;
-                    wv[1] = vw.y;
+                    const uint2 z = ld_s64(vb + 8 * n * vw);
+                    wv[0] = z.x;
+                    wv[1] = z.y;
                 }
 #pragma unroll
                 for (int x = 0; x < NS; ++x) {
@@ -465,6 +524,8 @@ __global__ void __launch_bounds__(Dc<D>::NW * 32, 1) kv8_decode_kernel(const Att
                 }
             }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[ci][hV % NSLOT]);
 
         // ---- the tile, or this warp's stretch of it, ends
         const bool tile_end = cc.c == cc.d.nc - 1;
@@ -574,12 +635,16 @@ constexpr int DEC_MAX_SMS = 160;
 template <int D>
 cudaError_t decode_launch(const AttnParams& P, int sms, cudaStream_t st) {
     using F = Dc<D>;
+    // slices of T keys of a page's V rows, where a page holds more
+    CUtensorMap vmap{};
+    const int64_t pg = (int64_t)1 << P.c.pshift;
+    if (pg > F::T && api_byte_map(&vmap, P.c.v, pg, D, P.c.n_pages * P.c.n_kv, F::T, D) != 0) return cudaErrorInvalidValue;
     const bool extra = P.softcap > 0.f || P.slopes;
     auto kern = extra ? kv8_decode_kernel<D, true> : kv8_decode_kernel<D, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
     if (e != cudaSuccess) return e;
     const int grid = sms < DEC_MAX_SMS ? sms : DEC_MAX_SMS;
-    kern<<<grid, F::NW * 32, F::SMEM, st>>>(P);
+    kern<<<grid, F::NT, F::SMEM, st>>>(P, vmap);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t c{};
     const int ty = P.s.ntok < 65535 ? P.s.ntok : 65535;
@@ -591,13 +656,13 @@ cudaError_t decode_launch(const AttnParams& P, int sms, cudaStream_t st) {
     at.val.programmaticStreamSerializationAllowed = 1;
     c.attrs = &at;
     c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, kv8_combine_kernel<D>, P, grid * F::NW);
+    return cudaLaunchKernelEx(&c, kv8_combine_kernel<D>, P, grid * F::NC);
 }
 
 }  // namespace
 
 size_t kv8_attn_workspace(int n_q, int n_kv, int d, int nseq, int ntok) {
-    const int nw = d == 64 ? Dc<64>::NW : d == 128 ? Dc<128>::NW : Dc<256>::NW;
+    const int nw = d == 64 ? Dc<64>::NC : d == 128 ? Dc<128>::NC : Dc<256>::NC;
     return base_bytes(nseq) + (size_t)DEC_MAX_SMS * nw * 2 * part_floats(d) * sizeof(float);
 }
 

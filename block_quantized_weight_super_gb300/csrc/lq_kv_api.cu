@@ -28,7 +28,8 @@ int page_shift(int page) {
 
 int check_cache(const lq_kv8* c, KvView& v) {
     if (!c) return api_fail(LQ_EINVAL, "cache is null");
-    if (c->n_pages < 1 || c->n_pages > INT32_MAX || c->n_kv < 1 || c->n_kv > 1024)
+    if (c->n_pages < 1 || c->n_pages > INT32_MAX || c->n_kv < 1 || c->n_kv > 1024 ||
+        c->n_pages * c->n_kv > INT32_MAX)
         return api_fail(LQ_ESHAPE, "cache: n_pages %lld n_kv %d", (long long)c->n_pages, (int)c->n_kv);
     const int s = page_shift(c->page);
     if (s < 0) return api_fail(LQ_ESHAPE, "cache: page %d (16, 32, 64, 128 or 256)", (int)c->page);
