@@ -17,18 +17,16 @@
 // 16-byte piece.  Four codes become two fp16 pairs in five instructions.
 //
 // Split.  (sequence, kv head, row tile, chunk) are numbered in one line and
-// dealt to the consumer warps of one CTA per SM in equal shares, whatever the
-// lengths; they never meet.  A warp keeps a running maximum, sum and O for its
-// stretch of a tile; a tile that spans several warps leaves one partial
-// result per warp and kv8_combine_kernel joins them in order.  The shares
-// depend on the lengths and the SM count only, so results are reproducible.
+// dealt to the warps of one CTA per SM in equal shares, whatever the lengths;
+// they never meet.  A warp keeps a running maximum, sum and O for its stretch
+// of a tile; a tile that spans several warps leaves one partial result per
+// warp and kv8_combine_kernel joins them in order.  The shares depend on the
+// lengths and the SM count only, so results are reproducible.
 //
-// Loads.  One warp more per CTA is the producer: its lane i walks consumer
-// i's share ahead of it, reads the page table and copies K, then V of each
-// chunk into the consumer's ring of half-chunks (bulk copies; a tensor copy
-// where a chunk is a slice of a page's V rows), with full / empty barriers.
-// That keeps addresses, page lookups and the copies' registers out of the
-// consumers, whose instruction issue is what limits them.
+// Loads.  Each warp streams its chunks through its own ring of half-chunks
+// (K, then V), always all but one of them in flight: bulk copies by its first
+// lanes, one per page (a tensor copy where a chunk is a slice of a page's V
+// rows).  The lanes hold the next 32 page indices of the table in a register.
 #include "lq_kv8_attn.cuh"
 
 namespace lq {
@@ -38,14 +36,14 @@ template <int D>
 struct Dc {
     static constexpr int T = D == 64 ? 64 : 32;              // keys of a chunk
     static constexpr int TQ = T / 4;                         // keys of a thread of a quad
-    static constexpr int NC = D == 64 ? 15 : D == 128 ? 11 : 7;    // consumer warps (with the producer 4, 3 or 2 per scheduler)
-    static constexpr int NT = (NC + 1) * 32;
-    static constexpr int NSLOT = D == 256 ? 2 : 3;   // half-chunks of a consumer's ring
+    static constexpr int NC = D == 64 ? 15 : D == 128 ? 12 : 8;    // warps: 4, 3 or 2 per scheduler, as registers allow
+    static constexpr int NT = NC * 32;
+    static constexpr int NSLOT = D == 256 ? 2 : 3;   // half-chunks of a warp's ring
     static constexpr int HB = T * D;                         // bytes of a half-chunk
     static constexpr int HBP = HB + 128;                     // with the padding between pages of V
     static constexpr int QB = D * 32;                        // q fragments
     static constexpr int NMETA = 4;                          // chunks whose scales are held
-    static constexpr int WB = NSLOT * HBP + QB + NMETA * 64; // shared memory of a consumer (a multiple of 128)
+    static constexpr int WB = NSLOT * HBP + QB + NMETA * 64; // shared memory of a warp (a multiple of 128)
     static constexpr int SMEM = NC * WB;
 };
 
@@ -147,13 +145,12 @@ __global__ void __launch_bounds__(Dc<D>::NT, 1) kv8_decode_kernel(const AttnPara
     constexpr int T = F::T, TQ = F::TQ, NS = TQ / 4, NT = F::NT, NC = F::NC, NSLOT = F::NSLOT;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t tb[NT];
-    __shared__ int64_t wsum[NC + 1];
-    __shared__ uint64_t full[NC][NSLOT], empty[NC][NSLOT];
+    __shared__ int64_t wsum[NC];
+    __shared__ uint64_t full[NC][NSLOT];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     pdl_launch_dependents();
     if (tid < NC * NSLOT) {
-        mbar_init(&full[0][0] + tid, 2);                  // the producer's two arrivals
-        mbar_init(&empty[0][0] + tid, 1);
+        mbar_init(&full[0][0] + tid, 1 + T / 16);         // the copies' bytes, the scales' lanes
         fence_mbar_init();
     }
 
@@ -170,7 +167,7 @@ __global__ void __launch_bounds__(Dc<D>::NT, 1) kv8_decode_kernel(const AttnPara
     if (lane == 31) wsum[warp] = inc;
     __syncthreads();
     int64_t before = 0, U = 0;
-    for (int i = 0; i < NC + 1; ++i) {
+    for (int i = 0; i < NC; ++i) {
         if (i < warp) before += wsum[i];
         U += wsum[i];
     }
@@ -186,16 +183,13 @@ __global__ void __launch_bounds__(Dc<D>::NT, 1) kv8_decode_kernel(const AttnPara
     }
     __syncthreads();
 
-    // consumers in use (none without a unit) and the one this thread works
-    // for; few units go to different SMs
-    const bool producer = warp == NC;
-    const int ci = producer ? min(lane, NC - 1) : warp;
-    const int W = (int)min((int64_t)gridDim.x * NC, U), w = ci * gridDim.x + blockIdx.x;
-    if (w >= W && !producer) return;
-    const int64_t u0 = w < W ? U * w / W : 0;
-    const int nu = w < W && (!producer || lane < NC) ? (int)(U * (w + 1) / W - u0) : 0;
-    Cur cc{};                                             // the unit at hand
-    if (nu > 0) {
+    // warps in use (none without a unit) and this one: few units go to different SMs
+    const int W = (int)min((int64_t)gridDim.x * NC, U), w = warp * gridDim.x + blockIdx.x;
+    if (w >= W) return;                                   // warps never meet again
+    const int64_t u0 = U * w / W;
+    const int nu = (int)(U * (w + 1) / W - u0);
+    Cur cc;                                               // the unit at hand
+    {
         const int i = kv_find(NT, u0, [&](int x) { return tb[x]; });
         int64_t b = tb[i];
         int s = i * per;
@@ -210,106 +204,64 @@ __global__ void __launch_bounds__(Dc<D>::NT, 1) kv8_decode_kernel(const AttnPara
         cc.tile = (int)(item % cc.d.tiles);
         cc.hk = (int)(item / cc.d.tiles);
     }
-    const uint32_t wbase = smem_u32(smem) + ci * F::WB, qbase = wbase + NSLOT * F::HBP, mbase = qbase + F::QB;
+    uint64_t* const bars = full[warp];
+    const uint32_t wbase = smem_u32(smem) + warp * F::WB, qbase = wbase + NSLOT * F::HBP, mbase = qbase + F::QB;
     const int pshift = P.c.pshift, Pg = 1 << pshift;
 
-    if (producer) {
-        const int pw = min(Pg, T), npg = T / pw;           // keys of a chunk per page, pages of a chunk
-        const int64_t blk = (int64_t)D << pshift;         // bytes of a page's head
-        const uint32_t pb = (uint32_t)pw * D, pad = npg > 1 ? 128u / npg : 0u;
-        int pg[4], nx[4];                                 // pages of this unit, of the next one
-        auto pages = [&](const Cur& k, int (&out)[4]) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int pos = cur_chunk(k) * T + i * pw;
-                out[i] = i < npg && pos < k.d.q.len ? att_page(P, k.d.q.s, pos) : -1;
-            }
-        };
-        Cur cn = cc;
-        if (nu > 0) {
-            pages(cc, pg);
-            if (nu > 1) {
-                cur_next<T>(P, cn);
-                pages(cn, nx);
-            }
-        }
-        int h = 0;
-        bool stop = nu == 0;
-        uint64_t idle0 = 0;                               // since when this lane has waited
-        while (__any_sync(0xFFFFFFFFu, !stop)) {
-            const int slot = h % NSLOT;
-            const bool go = !stop && (h < NSLOT || mbar_try_wait(&empty[ci][slot], (uint32_t)((h / NSLOT - 1) & 1)));
-            if (go) {
-                idle0 = 0;
-                uint64_t* bar = &full[ci][slot];
-                const uint32_t dst = wbase + slot * F::HBP;
-                int n = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) n += i < npg && pg[i] >= 0;
-                const int off = cur_chunk(cc) * T & (Pg - 1);               // the chunk's place in its page (npg = 1)
-                if ((h & 1) == 0) {
-                    const uint32_t m = mbase + (h / 2 % F::NMETA) * 64;
-#pragma unroll
-                    for (int i = 0; i < T / 16; ++i) {
-                        const int p = pg[npg == 1 ? 0 : i * 16 / pw];
-                        st_sf(m + 32 + 4 * i, p < 0 ? 0.f : 1.f);
-                        if (p < 0) {
-                            st_sf(m + 4 * i, 0.f);
-                            st_sf(m + 16 + 4 * i, 0.f);
-                        }
-                    }
-                    if (n > 0) mbar_arrive_expect_tx(bar, n * pb);
-                    else mbar_arrive(bar);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (i < npg && pg[i] >= 0)
-                            bulk_copy(dst + i * pb, P.c.k + ((int64_t)pg[i] * P.c.n_kv + cc.hk) * blk + (int64_t)off * D, pb, bar);
-#pragma unroll
-                    for (int i = 0; i < T / 16; ++i) {
-                        const int p = pg[npg == 1 ? 0 : i * 16 / pw];
-                        if (p >= 0) {
-                            cp4(m + 4 * i, P.c.ks + (int64_t)p * P.c.n_kv + cc.hk);
-                            cp4(m + 16 + 4 * i, P.c.vs + (int64_t)p * P.c.n_kv + cc.hk);
-                        }
-                    }
-                    cp_arrive(bar);
+    // ---- loading, ahead of the computation
+    Cur ci = cc;                                          // the unit to load
+    const int lpw = min(pshift, T == 64 ? 6 : 5), lnp = (T == 64 ? 6 : 5) - lpw;   // log2 of the keys a page gives a chunk, of its pages
+    int wc = ci.c, win = -1;                              // lane x: the page x & (pages - 1) of chunk wc + x / pages of this item
+    auto window = [&]() {
+        wc = ci.c;
+        Cur k = ci;
+        k.c += lane >> lnp;
+        const int pos = cur_chunk(k) * T + ((lane & ((1 << lnp) - 1)) << lpw);
+        win = k.c < k.d.nc && pos < k.d.q.len ? att_page(P, k.d.q.s, pos) : -1;
+    };
+    window();
+    auto issue = [&](int h) {                             // half-chunk h: K (even) or V (odd) of unit h / 2
+        if (h >= 2 * nu) return;
+        const int slot = h % NSLOT, np = 1 << lnp;
+        uint64_t* bar = bars + slot;
+        const uint32_t dst = wbase + slot * F::HBP, pb = (uint32_t)D << lpw;
+        const int pg = __shfl_sync(0xFFFFFFFFu, win, ((ci.c - wc) << lnp) + (lane & (np - 1)));   // lane i: the chunk's page i
+        const int pm = __shfl_sync(0xFFFFFFFFu, pg, (lane & 3) << 4 >> lpw);   // lane i: the page of the chunk's i-th 16 keys
+        const bool have = lane < np && pg >= 0;
+        const int n = __popc(__ballot_sync(0xFFFFFFFFu, have));
+        const int off = cur_chunk(ci) * T & (Pg - 1);     // the chunk's place in its page (0 unless it is a part of it)
+        const int64_t ph = (int64_t)pg * P.c.n_kv + ci.hk;
+        if ((h & 1) == 0) {
+            if (lane < T / 16) {
+                const uint32_t m = mbase + (h / 2 % F::NMETA) * 64 + 4 * lane;
+                st_sf(m + 32, pm < 0 ? 0.f : 1.f);
+                if (pm < 0) {
+                    st_sf(m, 0.f);
+                    st_sf(m + 16, 0.f);
                 } else {
-                    if (n > 0) mbar_arrive_expect_tx(bar, n * pb);
-                    else mbar_arrive(bar);
-                    mbar_arrive(bar);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (i < npg && pg[i] >= 0) {
-                            const int64_t ph = (int64_t)pg[i] * P.c.n_kv + cc.hk;
-                            if (pw == Pg) bulk_copy(dst + i * (pb + pad), P.c.v + ph * blk, pb, bar);
-                            else tma_load_3d(dst, &vmap, off, 0, (int)ph, bar);
-                        }
-                    // the next unit, whose pages are here, and the pages of the one behind it
-                    cc = cn;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) pg[i] = nx[i];
-                    if (h / 2 + 2 < nu) {
-                        cur_next<T>(P, cn);
-                        pages(cn, nx);
-                    }
+                    cp4(m, P.c.ks + (int64_t)pm * P.c.n_kv + ci.hk);
+                    cp4(m + 16, P.c.vs + (int64_t)pm * P.c.n_kv + ci.hk);
                 }
-                stop = ++h == 2 * nu;
-            } else if (!stop) {
-                const uint64_t now = globaltimer_ns();
-                if (idle0 == 0) {
-                    idle0 = now;
-                } else if (now - idle0 > P.timeout_ns) {
-                    record_status(P.status, STATUS_TIMEOUT);
-                    stop = true;
-                }
+                cp_arrive(bar);
+            }
+            if (have) bulk_copy(dst + lane * pb, P.c.k + ((ph * D) << pshift) + (int64_t)off * D, pb, bar);
+        } else {
+            if (lane < T / 16) mbar_arrive(bar);
+            if (have) {
+                if (lpw == pshift) bulk_copy(dst + lane * (pb + (lnp ? 128 >> lnp : 0)), P.c.v + ((ph * D) << pshift), pb, bar);
+                else tma_load_3d(dst, &vmap, off, 0, (int)ph, bar);
             }
         }
-        // the last copies have landed before the CTA may exit
-        for (int k = max(0, h - NSLOT); k < h; ++k)
-            if (!mbar_wait_bounded(&full[ci][k % NSLOT], (uint32_t)((k / NSLOT) & 1), drain_bound(P.timeout_ns)))
-                record_status(P.status, STATUS_TIMEOUT);
-        return;
-    }
+        if (lane == 0) {
+            if (n > 0) mbar_arrive_expect_tx(bar, n * pb);
+            else mbar_arrive(bar);
+        }
+        if ((h & 1) && h / 2 + 1 < nu) {
+            cur_next<T>(P, ci);
+            if (ci.c == 0 || ci.c - wc >= 32 >> lnp) window();
+        }
+    };
+    for (int h = 0; h < NSLOT - 1; ++h) issue(h);
 
     const int grp = P.n_q / P.c.n_kv;
     float* part = reinterpret_cast<float*>(P.ws + base_bytes(P.s.nseq));
@@ -323,6 +275,16 @@ __global__ void __launch_bounds__(Dc<D>::NT, 1) kv8_decode_kernel(const AttnPara
     int head = 0;
     float is = 1.f;                                       // 2^-e0
 
+    // Waits for half-chunk h; every lane is past the half before it then,
+    // whose slot is the next to fill.  On a timeout the halves in flight
+    // still land (bounded) before the warp leaves.
+    auto arrived = [&](int h) -> bool {
+        if (__all_sync(0xFFFFFFFFu, mbar_wait_bounded(bars + h % NSLOT, (uint32_t)((h / NSLOT) & 1), P.timeout_ns))) return true;
+        record_status(P.status, STATUS_TIMEOUT);
+        for (int k = h; k < min(h + NSLOT - 1, 2 * nu); ++k)
+            mbar_wait_bounded(bars + k % NSLOT, (uint32_t)((k / NSLOT) & 1), drain_bound(P.timeout_ns));
+        return false;
+    };
     for (int u = 0; u < nu; ++u) {
         const AttSeq& q = cc.d.q;
         if (fresh) {
@@ -387,10 +349,8 @@ __global__ void __launch_bounds__(Dc<D>::NT, 1) kv8_decode_kernel(const AttnPara
 
         // ---- S = Q K^T
         const int hK = 2 * u;
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[ci][hK % NSLOT], (uint32_t)((hK / NSLOT) & 1), P.timeout_ns))) {
-            record_status(P.status, STATUS_TIMEOUT);
-            return;
-        }
+        if (!arrived(hK)) return;
+        issue(hK + NSLOT - 1);
         const uint32_t mt = mbase + (u % F::NMETA) * 64 + (TQ * t / 16) * 4;
         const float ks = ld_sf(mt), vs = ld_sf(mt + 16);
         const bool held = ld_sf(mt + 32) != 0.f;
@@ -429,8 +389,6 @@ __global__ void __launch_bounds__(Dc<D>::NT, 1) kv8_decode_kernel(const AttnPara
                     }
             }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[ci][hK % NSLOT]);
 
         // ---- weights
         const int j0 = cur_chunk(cc) * T, jt = j0 + TQ * t;
@@ -496,10 +454,8 @@ __global__ void __launch_bounds__(Dc<D>::NT, 1) kv8_decode_kernel(const AttnPara
 
         // ---- O += W V
         const int hV = hK + 1;
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[ci][hV % NSLOT], (uint32_t)((hV / NSLOT) & 1), P.timeout_ns))) {
-            record_status(P.status, STATUS_TIMEOUT);
-            return;
-        }
+        if (!arrived(hV)) return;
+        issue(hV + NSLOT - 1);
         {
             const uint32_t vb = wbase + (hV % NSLOT) * F::HBP + voff;
 #pragma unroll
@@ -524,8 +480,6 @@ __global__ void __launch_bounds__(Dc<D>::NT, 1) kv8_decode_kernel(const AttnPara
                 }
             }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[ci][hV % NSLOT]);
 
         // ---- the tile, or this warp's stretch of it, ends
         const bool tile_end = cc.c == cc.d.nc - 1;
