@@ -21,6 +21,17 @@ __device__ __forceinline__ float att_ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ float att_lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float att_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // tanh to fp32 rounding: an odd polynomial (least-squares fit of tanh(x) / x
 // in x^2, relative error 3e-9) up to 0.6, where 1 - 2 / (e^2x + 1) would
 // cancel, and that form beyond (its error is then below 2^-23 of the value).
@@ -49,12 +60,8 @@ __device__ __forceinline__ void att_split(float x, float y, uint32_t& hi, uint32
 // fp16 0x64xx reads 1024 + 128 + code.
 __device__ __forceinline__ void att_codes(uint32_t w, uint32_t& a, uint32_t& b) {
     const uint32_t u = w ^ 0x80808080u;
-    const __half2 off = __half2half2(__ushort_as_half(0x6480));     // 1152
-    const uint32_t x = prmt(u, 0x64646464u, 0x4140u), y = prmt(u, 0x64646464u, 0x4342u);
-    const __half2 p = __hsub2(*reinterpret_cast<const __half2*>(&x), off);
-    const __half2 q = __hsub2(*reinterpret_cast<const __half2*>(&y), off);
-    a = *reinterpret_cast<const uint32_t*>(&p);
-    b = *reinterpret_cast<const uint32_t*>(&q);
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(a) : "r"(prmt(u, 0x64646464u, 0x4140u)), "r"(0xE480E480u));
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(b) : "r"(prmt(u, 0x64646464u, 0x4342u)), "r"(0xE480E480u));
 }
 
 // What a sequence's query rows can see: keys below len; all of them [0, pre)
@@ -78,11 +85,6 @@ __device__ __forceinline__ AttSeq att_seq(const AttnParams& P, int s) {
     const int64_t p0 = max(q.start, (int64_t)0);
     q.lo = P.window ? (int)min(max(p0 - P.window + 1, (int64_t)0), (int64_t)q.len) : 0;
     return q;
-}
-
-// Whether the query at position p sees key j (j < len).
-__device__ __forceinline__ bool att_sees(const AttnParams& P, const AttSeq& q, int p, int j) {
-    return j < q.len && p >= 0 && (j < q.pre || (j <= p && (P.window == 0 || p - j < P.window)));
 }
 
 // The page of a sequence's position, -1 if there is none.

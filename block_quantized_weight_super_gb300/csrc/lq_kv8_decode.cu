@@ -2,19 +2,23 @@
 // per sequence (decoding): bound by the HBM reads of the codes.
 //
 // Rows.  The query rows of one kv head (tokens x the heads of its group) are
-// taken 8 at a time.  mma.sync.m16n8k16 with A = those 8 rows as fp16 hi
-// pieces (A rows 0-7) and lo pieces (8-15): the two halves of a D fragment lie
-// in one thread and their sum is the fp32-accurate product, for the price of
-// the M = 16 tile that 8 rows would cost anyway.  B = the codes, exact in
-// fp16: S = Q K^T takes 8 keys x 16 dims per MMA, O += W V 16 keys x 8 dims.
-// The D fragment of S (row g, keys 2t, 2t + 1) is the A fragment of the second
-// product, so the weights never leave the thread.
+// taken 4 or 8 at a time.  mma.sync.m16n8k16 with the codes as A, exact in
+// fp16, and the rows as B: columns 2t and 2t + 1 are the hi and the lo fp16
+// piece of row t, so a column pair of D, which lies in one thread, sums to the
+// fp32-accurate product and no part of the tile is idle.  S^T = K Q^T takes
+// 16 keys x 16 dims per MMA, O^T += V^T W^T 16 dims x 16 keys.  Thread t of a
+// quad has row t in both products: its running maximum and sum, its weights
+// and its part of O never leave it, except that the weights' (hi, lo) pairs,
+// as a D fragment lays them out, go through an 8 x 8 transpose (movmatrix) to
+// become the B fragment of the second product.
 //
-// Keys.  Thread t of a quad owns T / 4 adjacent keys of a T-key chunk (the
-// key a column stands for is free to choose): they lie in one page, so both
-// scales are one register per thread, the K bytes of a key are 16-byte pieces
-// and the V bytes of a dim (pages hold V with the tokens adjacent) one 8- or
-// 16-byte piece.  Four codes become two fp16 pairs in five instructions.
+// Keys.  Which key a row of the tile stands for is free to choose: quad pair q
+// (= g / 2 in the first product, t in the second) owns T / 4 adjacent keys of
+// a T-key chunk.  They lie in one page, so both scales are one register per
+// thread; the K bytes of a key are 16-byte pieces and the V bytes of a dim
+// (pages hold V with the tokens adjacent) one 8- or 16-byte piece.  Four
+// codes become two fp16 pairs in five instructions: at 6.8 TB/s these are a
+// quarter of the SMs' issue slots, the rest of a chunk's work a fifth.
 //
 // Split.  (sequence, kv head, row tile, chunk) are numbered in one line and
 // dealt to the warps of one CTA per SM in equal shares, whatever the lengths;
@@ -32,23 +36,31 @@
 namespace lq {
 namespace {
 
-template <int D>
+template <int D, int NR>                                     // NR: row quads of a tile (1 or 2)
 struct Dc {
+    static constexpr int RT = 4 * NR;                        // rows of a tile
     static constexpr int T = D == 64 ? 64 : 32;              // keys of a chunk
-    static constexpr int TQ = T / 4;                         // keys of a thread of a quad
-    static constexpr int NC = D == 64 ? 15 : D == 128 ? 12 : 8;    // warps: 4, 3 or 2 per scheduler, as registers allow
+    static constexpr int TQ = T / 4;                         // keys of a quad pair
+    static constexpr int NX = T / 16;                        // 16-key MMA tiles of a chunk
+    // warps: 2 to 4 per scheduler, as registers allow
+    static constexpr int NC = NR == 1 ? (D == 256 ? 10 : 16) : (D == 256 ? 8 : 12);
     static constexpr int NT = NC * 32;
-    static constexpr int NSLOT = D == 256 ? 2 : 3;   // half-chunks of a warp's ring
+    static constexpr int NSLOT = D == 256 ? 2 : 3;           // half-chunks of a warp's ring
     static constexpr int HB = T * D;                         // bytes of a half-chunk
     static constexpr int HBP = HB + 128;                     // with the padding between pages of V
-    static constexpr int QB = D * 32;                        // q fragments
+    static constexpr bool QS = D == 256;                    // q fragments in shared memory (registers are full)
+    static constexpr int QB = QS ? D * 16 * NR : 0;
     static constexpr int NMETA = 4;                          // chunks whose scales are held
-    static constexpr int WB = NSLOT * HBP + QB + NMETA * 64; // shared memory of a warp (a multiple of 128)
+    static constexpr int WB = NSLOT * HBP + QB + NMETA * 32; // shared memory of a warp (a multiple of 128)
     static constexpr int SMEM = NC * WB;
 };
+constexpr int MAX_RT = 8;
 
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 // Arrives on the barrier (one of its expected arrivals) once this thread's
 // cp.async so far have landed.
@@ -89,17 +101,38 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The same with C = 0.
+__device__ __forceinline__ void mma16816_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%10, %10, %10, %10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// 8 x 8 fp16 transpose across the warp (row g, columns 2t, 2t + 1 per thread).
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+// The fp16 pieces of one value, hi in the low half.
+__device__ __forceinline__ uint32_t split1(float w) {
+    const __half h = __float2half_rn(w);
+    const __half2 p = __halves2half2(h, __float2half_rn(w - __half2float(h)));
+    return *reinterpret_cast<const uint32_t*>(&p);
+}
+
 // A sequence as the split sees it: `tiles` row tiles per kv head, each over
 // the same nc chunks: the first na, then those from cb on.
 struct DecSeq {
     AttSeq q;
     int32_t tiles, na, cb, nc;
 };
-template <int T>
+template <int T, int RT>
 __device__ __forceinline__ DecSeq dec_seq(const AttnParams& P, int s) {
     DecSeq d;
     d.q = att_seq(P, s);
-    d.tiles = (int)(((int64_t)d.q.n * (P.n_q / P.c.n_kv) + 7) >> 3);
+    d.tiles = (int)(((int64_t)d.q.n * (P.n_q / P.c.n_kv) + RT - 1) / RT);
     const int ce = (d.q.len + T - 1) / T;
     d.cb = min(d.q.lo / T, ce);
     d.na = min((d.q.pre + T - 1) / T, d.cb);
@@ -115,7 +148,7 @@ struct Cur {
     DecSeq d;
     int32_t hk, tile, c;
 };
-template <int T>
+template <int T, int RT>
 __device__ __forceinline__ void cur_next(const AttnParams& P, Cur& k) {
     if (++k.c < k.d.nc) return;
     k.c = 0;
@@ -125,24 +158,24 @@ __device__ __forceinline__ void cur_next(const AttnParams& P, Cur& k) {
     k.hk = 0;
     int s = k.d.q.s + 1;
     for (; s < P.s.nseq; ++s) {
-        k.d = dec_seq<T>(P, s);
+        k.d = dec_seq<T, RT>(P, s);
         if (dec_units(P, k.d) > 0) return;
     }
 }
 __device__ __forceinline__ int cur_chunk(const Cur& k) { return k.c < k.d.na ? k.c : k.d.cb + (k.c - k.d.na); }
 
 // Workspace: base [nseq + 1] int64 (padded), then the partial results:
-// 2 per worker, [8 rows][D] of O, then [8][2] of (max, sum).
-__host__ __device__ constexpr int64_t part_floats(int d) { return 8 * (int64_t)d + 16; }
+// 2 per worker, [MAX_RT rows][D] of O, then [MAX_RT][2] of (max, sum).
+__host__ __device__ constexpr int64_t part_floats(int d) { return MAX_RT * (int64_t)d + 2 * MAX_RT; }
 __host__ __device__ inline size_t base_bytes(int nseq) { return ((size_t)(nseq + 1) * 8 + 255) & ~size_t(255); }
 
 // First worker of W whose share [U w / W, U (w + 1) / W) holds unit u.
 __device__ __forceinline__ int owner(int64_t u, int64_t U, int W) { return (int)(((u + 1) * W - 1) / U); }
 
-template <int D, bool EXTRA>
-__global__ void __launch_bounds__(Dc<D>::NT, 1) kv8_decode_kernel(const AttnParams P, const __grid_constant__ CUtensorMap vmap) {
-    using F = Dc<D>;
-    constexpr int T = F::T, TQ = F::TQ, NS = TQ / 4, NT = F::NT, NC = F::NC, NSLOT = F::NSLOT;
+template <int D, int NR, bool EXTRA>
+__global__ void __launch_bounds__(Dc<D, NR>::NT, 1) kv8_decode_kernel(const AttnParams P, const __grid_constant__ CUtensorMap vmap) {
+    using F = Dc<D, NR>;
+    constexpr int T = F::T, TQ = F::TQ, NX = F::NX, NT = F::NT, NC = F::NC, NSLOT = F::NSLOT, RT = F::RT;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t tb[NT];
     __shared__ int64_t wsum[NC];
@@ -150,14 +183,15 @@ __global__ void __launch_bounds__(Dc<D>::NT, 1) kv8_decode_kernel(const AttnPara
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     pdl_launch_dependents();
     if (tid < NC * NSLOT) {
-        mbar_init(&full[0][0] + tid, 1 + T / 16);         // the copies' bytes, the scales' lanes
+        // an arrival for each page of a chunk
+        mbar_init(&full[0][0] + tid, P.c.pshift == 4 ? T / 16 : P.c.pshift == 5 ? T / 32 : max(1, T >> P.c.pshift));
         fence_mbar_init();
     }
 
     // ---- the line: thread i sums the units of its sequences
     const int per = (P.s.nseq + NT - 1) / NT;
     int64_t mine = 0;
-    for (int s = tid * per; s < min((tid + 1) * per, P.s.nseq); ++s) mine += dec_units(P, dec_seq<T>(P, s));
+    for (int s = tid * per; s < min((tid + 1) * per, P.s.nseq); ++s) mine += dec_units(P, dec_seq<T, RT>(P, s));
     int64_t inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -177,7 +211,7 @@ __global__ void __launch_bounds__(Dc<D>::NT, 1) kv8_decode_kernel(const AttnPara
         int64_t b = before + inc - mine;
         for (int s = tid * per; s < min((tid + 1) * per, P.s.nseq); ++s) {
             base[s] = b;
-            b += dec_units(P, dec_seq<T>(P, s));
+            b += dec_units(P, dec_seq<T, RT>(P, s));
         }
         if (tid == 0) base[P.s.nseq] = U;
     }
@@ -194,7 +228,7 @@ __global__ void __launch_bounds__(Dc<D>::NT, 1) kv8_decode_kernel(const AttnPara
         int64_t b = tb[i];
         int s = i * per;
         for (;; ++s) {
-            cc.d = dec_seq<T>(P, s);
+            cc.d = dec_seq<T, RT>(P, s);
             const int64_t n = dec_units(P, cc.d);
             if (b + n > u0) break;
             b += n;
@@ -211,53 +245,52 @@ __global__ void __launch_bounds__(Dc<D>::NT, 1) kv8_decode_kernel(const AttnPara
     // ---- loading, ahead of the computation
     Cur ci = cc;                                          // the unit to load
     const int lpw = min(pshift, T == 64 ? 6 : 5), lnp = (T == 64 ? 6 : 5) - lpw;   // log2 of the keys a page gives a chunk, of its pages
-    int wc = ci.c, win = -1;                              // lane x: the page x & (pages - 1) of chunk wc + x / pages of this item
+    // Lane x looks after page x & (pages - 1) of chunk wc + x / pages of this
+    // item: (page, head) in `win`, -1 if there is none.  It issues that page's
+    // copies itself, so issuing takes no shuffles.
+    int wc = ci.c, win = -1;
+    const int wl = lane >> lnp, wi = lane & ((1 << lnp) - 1);
     auto window = [&]() {
         wc = ci.c;
         Cur k = ci;
-        k.c += lane >> lnp;
-        const int pos = cur_chunk(k) * T + ((lane & ((1 << lnp) - 1)) << lpw);
-        win = k.c < k.d.nc && pos < k.d.q.len ? att_page(P, k.d.q.s, pos) : -1;
+        k.c += wl;
+        const int pos = cur_chunk(k) * T + (wi << lpw);
+        const int pg = k.c < k.d.nc && pos < k.d.q.len ? att_page(P, k.d.q.s, pos) : -1;
+        win = pg < 0 ? -1 : pg * P.c.n_kv + ci.hk;
     };
     window();
+    const uint32_t pb = (uint32_t)D << lpw, blk = (uint32_t)D << pshift;      // bytes of a copy; of a page's head
+    const uint32_t vpad = lnp ? 128u >> lnp : 0u;
+    int hs = 0;                                           // slot of the half-chunk to load
     auto issue = [&](int h) {                             // half-chunk h: K (even) or V (odd) of unit h / 2
         if (h >= 2 * nu) return;
-        const int slot = h % NSLOT, np = 1 << lnp;
-        uint64_t* bar = bars + slot;
-        const uint32_t dst = wbase + slot * F::HBP, pb = (uint32_t)D << lpw;
-        const int pg = __shfl_sync(0xFFFFFFFFu, win, ((ci.c - wc) << lnp) + (lane & (np - 1)));   // lane i: the chunk's page i
-        const int pm = __shfl_sync(0xFFFFFFFFu, pg, (lane & 3) << 4 >> lpw);   // lane i: the page of the chunk's i-th 16 keys
-        const bool have = lane < np && pg >= 0;
-        const int n = __popc(__ballot_sync(0xFFFFFFFFu, have));
-        const int off = cur_chunk(ci) * T & (Pg - 1);     // the chunk's place in its page (0 unless it is a part of it)
-        const int64_t ph = (int64_t)pg * P.c.n_kv + ci.hk;
-        if ((h & 1) == 0) {
-            if (lane < T / 16) {
-                const uint32_t m = mbase + (h / 2 % F::NMETA) * 64 + 4 * lane;
-                st_sf(m + 32, pm < 0 ? 0.f : 1.f);
-                if (pm < 0) {
-                    st_sf(m, 0.f);
+        if (ci.c - wc == wl) {
+            uint64_t* bar = bars + hs;
+            const uint32_t dst = wbase + hs * F::HBP;
+            const int off = cur_chunk(ci) * T & (Pg - 1); // the chunk's place in its page (0 unless it is a part of it)
+            if ((h & 1) == 0) {
+                const uint32_t m = mbase + (h / 2 % F::NMETA) * 32 + 4 * wi;
+                if (win < 0) {
+                    st_sf(m, -1.f);                       // no such keys
                     st_sf(m + 16, 0.f);
                 } else {
-                    cp4(m, P.c.ks + (int64_t)pm * P.c.n_kv + ci.hk);
-                    cp4(m + 16, P.c.vs + (int64_t)pm * P.c.n_kv + ci.hk);
+                    cp4(m, P.c.ks + win);
+                    cp4(m + 16, P.c.vs + win);
+                    mbar_expect_tx(bar, pb);
+                    bulk_copy(dst + wi * pb, P.c.k + (int64_t)win * blk + off * D, pb, bar);
                 }
                 cp_arrive(bar);
-            }
-            if (have) bulk_copy(dst + lane * pb, P.c.k + ((ph * D) << pshift) + (int64_t)off * D, pb, bar);
-        } else {
-            if (lane < T / 16) mbar_arrive(bar);
-            if (have) {
-                if (lpw == pshift) bulk_copy(dst + lane * (pb + (lnp ? 128 >> lnp : 0)), P.c.v + ((ph * D) << pshift), pb, bar);
-                else tma_load_3d(dst, &vmap, off, 0, (int)ph, bar);
+            } else if (win < 0) {
+                mbar_arrive(bar);
+            } else {
+                mbar_arrive_expect_tx(bar, pb);
+                if (lpw == pshift) bulk_copy(dst + wi * (pb + vpad), P.c.v + (int64_t)win * blk, pb, bar);
+                else tma_load_3d(dst, &vmap, off, 0, win, bar);
             }
         }
-        if (lane == 0) {
-            if (n > 0) mbar_arrive_expect_tx(bar, n * pb);
-            else mbar_arrive(bar);
-        }
+        hs = hs + 1 == NSLOT ? 0 : hs + 1;
         if ((h & 1) && h / 2 + 1 < nu) {
-            cur_next<T>(P, ci);
+            cur_next<T, RT>(P, ci);
             if (ci.c == 0 || ci.c - wc >= 32 >> lnp) window();
         }
     };
@@ -266,20 +299,27 @@ __global__ void __launch_bounds__(Dc<D>::NT, 1) kv8_decode_kernel(const AttnPara
     const int grp = P.n_q / P.c.n_kv;
     float* part = reinterpret_cast<float*>(P.ws + base_bytes(P.s.nseq));
     const int vw = min(Pg, T);                            // keys per row of V in shared memory
-    const uint32_t voff = (uint32_t)(TQ * t / vw) * ((uint32_t)vw * D + (vw < T ? 128u / (T / vw) : 0u)) + (TQ * t) % vw + g * vw;
-    float o[D / 8][4];
-    float m = -INFINITY, l = 0.f, qs = 0.f, slope = 0.f;
-    int p = 0, e0 = 0;
-    bool rowok = false, fresh = true, from_start = false;
-    int64_t qrow = 0;
-    int head = 0;
+    const uint32_t voff = (uint32_t)(TQ * t / vw) * ((uint32_t)vw * D + vpad) + (TQ * t) % vw + g * vw;
+    const uint32_t koff = (TQ * (g >> 1) + (g & 1)) * D + 16 * t, moff = (uint32_t)(TQ * (g >> 1) >> lpw) * 4;
+    float o[D / 16][NR][4];
+    uint32_t qf[F::QS ? 1 : D / 16][NR][2];
+    // of this thread's row t of each quad: maximum, sum, scale of the score,
+    // slope, position, and the keys it sees, [vlo, vhi) and [0, vpre)
+    float m[NR], l[NR], qs[NR], slope[NR];
+    int p[NR], vlo[NR], vhi[NR], vpre[NR];
+    int e0 = 0;
     float is = 1.f;                                       // 2^-e0
+    bool fresh = true, from_start = false;
 
     // Waits for half-chunk h; every lane is past the half before it then,
     // whose slot is the next to fill.  On a timeout the halves in flight
     // still land (bounded) before the warp leaves.
+    int cs = NSLOT - 1;                                   // slot of the half-chunk at hand, and its phase
+    uint32_t cph = 1;
     auto arrived = [&](int h) -> bool {
-        if (__all_sync(0xFFFFFFFFu, mbar_wait_bounded(bars + h % NSLOT, (uint32_t)((h / NSLOT) & 1), P.timeout_ns))) return true;
+        cs = cs + 1 == NSLOT ? 0 : cs + 1;
+        cph ^= cs == 0;
+        if (__all_sync(0xFFFFFFFFu, mbar_wait_bounded(bars + cs, cph, P.timeout_ns))) return true;
         record_status(P.status, STATUS_TIMEOUT);
         for (int k = h; k < min(h + NSLOT - 1, 2 * nu); ++k)
             mbar_wait_bounded(bars + k % NSLOT, (uint32_t)((k / NSLOT) & 1), drain_bound(P.timeout_ns));
@@ -291,192 +331,240 @@ __global__ void __launch_bounds__(Dc<D>::NT, 1) kv8_decode_kernel(const AttnPara
             // ---- a tile begins (or this warp's stretch of it): its rows
             fresh = false;
             from_start = cc.c == 0;
-            const int r = cc.tile * 8 + g;
-            rowok = r < q.n * grp;
-            const int i = rowok ? r / grp : 0;
-            head = cc.hk * grp + (rowok ? r % grp : 0);
-            qrow = q.row0 + i;
-            p = (int)min(max(q.start + i, (int64_t)-1), (int64_t)INT32_MAX - 1);
-            const float* x = P.q + qrow * P.ld_q + (int64_t)head * D + 16 * t;
             const int pe = att_page(P, q.s, cc.d.na > 0 ? 0 : min(cc.d.cb * T, q.len - 1));
-            // the row's largest |q| and its power of two
-            float mx = 0.f;
-            float v[D / 64][16];
             const bool vec = ((reinterpret_cast<uintptr_t>(P.q) | (P.ld_q * 4)) & 15) == 0;
+            if (F::QS) __syncwarp();                      // every lane has read the last tile's fragments
 #pragma unroll
-            for (int a = 0; a < D / 64; ++a)
+            for (int z = 0; z < NR; ++z) {
+                // fragments: this thread makes the hi (g even) or lo piece of row g / 2
+                const int r = cc.tile * RT + 4 * z + (g >> 1);
+                const bool ok = r < q.n * grp;
+                const float* x = P.q + (int64_t)(q.row0 + (ok ? r / grp : 0)) * P.ld_q +
+                                 (int64_t)(cc.hk * grp + (ok ? r % grp : 0)) * D + 16 * t;
+                float mx = 0.f;
+                float v[D / 64][16];
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-                    const float* y = x + 64 * a + e;
-                    if (rowok) z = vec ? __ldg(reinterpret_cast<const float4*>(y)) : make_float4(__ldg(y), __ldg(y + 1), __ldg(y + 2), __ldg(y + 3));
-                    v[a][e] = z.x;
-                    v[a][e + 1] = z.y;
-                    v[a][e + 2] = z.z;
-                    v[a][e + 3] = z.w;
-                }
-            slope = P.slopes ? __ldg(P.slopes + head) : 0.f;
+                for (int a = 0; a < D / 64; ++a)
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) {
+                        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                        const float* y = x + 64 * a + e;
+                        if (ok) f = vec ? __ldg(reinterpret_cast<const float4*>(y)) : make_float4(__ldg(y), __ldg(y + 1), __ldg(y + 2), __ldg(y + 3));
+                        v[a][e] = f.x;
+                        v[a][e + 1] = f.y;
+                        v[a][e + 2] = f.z;
+                        v[a][e + 3] = f.w;
+                    }
+#pragma unroll
+                for (int a = 0; a < D / 64; ++a)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) mx = fmaxf(mx, fabsf(v[a][e]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+                // the row's power of two: |q| / 2^(es - 127) < 2^15
+                const int es = max(1, (int)((__float_as_uint(mx) >> 23) & 0xFFu) - 14);
+                const float inv = __uint_as_float((uint32_t)(254 - es) << 23);
+                qs[z] = __uint_as_float((uint32_t)__shfl_sync(0xFFFFFFFFu, es, 8 * t) << 23) * P.scale;   // of row t
+#pragma unroll
+                for (int a = 0; a < D / 64; ++a)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {         // MMA step 4 a + k: dims 64 a + 16 t + 4 k .. + 3
+                        uint32_t f[2], lo[2];
+                        att_split(v[a][4 * k] * inv, v[a][4 * k + 1] * inv, f[0], lo[0]);
+                        att_split(v[a][4 * k + 2] * inv, v[a][4 * k + 3] * inv, f[1], lo[1]);
+                        if (g & 1) {
+                            f[0] = lo[0];
+                            f[1] = lo[1];
+                        }
+                        if (F::QS) {
+                            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qbase + (((4 * a + k) * NR + z) * 32 + lane) * 8),
+                                         "r"(f[0]), "r"(f[1])
+                                         : "memory");     // (read back by this lane alone)
+                        } else {
+                            qf[F::QS ? 0 : 4 * a + k][z][0] = f[0];
+                            qf[F::QS ? 0 : 4 * a + k][z][1] = f[1];
+                        }
+                    }
+                // the softmax of row t
+                const int rt = cc.tile * RT + 4 * z + t;
+                const bool rok = rt < q.n * grp;
+                p[z] = (int)min(max(q.start + (rok ? rt / grp : 0), (int64_t)-1), (int64_t)INT32_MAX - 1);
+                vhi[z] = !rok ? INT32_MAX : p[z] < 0 ? 0 : min(p[z] + 1, q.len);
+                vlo[z] = rok && P.window ? max(p[z] - P.window + 1, 0) : 0;
+                vpre[z] = rok && p[z] >= 0 ? q.pre : 0;
+                slope[z] = EXTRA && P.slopes ? __ldg(P.slopes + cc.hk * grp + (rok ? rt % grp : 0)) : 0.f;
+                m[z] = -INFINITY;
+                l[z] = 0.f;
+            }
             e0 = pe >= 0 ? att_e0(__ldg(P.c.vs + (int64_t)pe * P.c.n_kv + cc.hk)) : 0;
             is = att_pow2(-e0);
 #pragma unroll
-            for (int a = 0; a < D / 64; ++a)
+            for (int n = 0; n < D / 16; ++n)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) mx = fmaxf(mx, fabsf(v[a][e]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-            const int es = max(1, (int)((__float_as_uint(mx) >> 23) & 0xFFu) - 14);
-            const float inv = __uint_as_float((uint32_t)(254 - es) << 23);
-            qs = __uint_as_float((uint32_t)es << 23) * P.scale;
-            __syncwarp();                                 // every lane has read the last tile's fragments
+                for (int z = 0; z < NR; ++z)
 #pragma unroll
-            for (int a = 0; a < D / 64; ++a)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {             // MMA step 4 a + k: dims 64 a + 16 t + 4 k .. + 3
-                    uint32_t f[4];
-                    att_split(v[a][4 * k] * inv, v[a][4 * k + 1] * inv, f[0], f[1]);
-                    att_split(v[a][4 * k + 2] * inv, v[a][4 * k + 3] * inv, f[2], f[3]);
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(qbase + ((4 * a + k) * 32 + lane) * 16),
-                                 "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3])
-                                 : "memory");             // (read back by this lane alone)
-                }
-            m = -INFINITY;
-            l = 0.f;
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                for (int z = 0; z < 4; ++z) o[n][z] = 0.f;
+                    for (int e = 0; e < 4; ++e) o[n][z][e] = 0.f;
         }
 
-        // ---- S = Q K^T
+        // ---- S^T = K Q^T
         const int hK = 2 * u;
         if (!arrived(hK)) return;
         issue(hK + NSLOT - 1);
-        const uint32_t mt = mbase + (u % F::NMETA) * 64 + (TQ * t / 16) * 4;
+        const uint32_t mt = mbase + (u % F::NMETA) * 32 + moff;
         const float ks = ld_sf(mt), vs = ld_sf(mt + 16);
-        const bool held = ld_sf(mt + 32) != 0.f;
-        float s[NS][2][4];
-#pragma unroll
-        for (int x = 0; x < NS; ++x)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int z = 0; z < 4; ++z) s[x][j][z] = 0.f;
+        const bool held = !(ks < 0.f);
+        float s[NX][NR][4];
         {
-            const uint32_t kb = wbase + (hK % NSLOT) * F::HBP + (TQ * (g >> 1) + (g & 1)) * D + 16 * t;
+            const uint32_t kb = wbase + cs * F::HBP + koff;
 #pragma unroll
             for (int a = 0; a < D / 64; ++a) {
-                uint32_t qa[4][4];
+                uint32_t qa[4][NR][2];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint4 f = ld_s128(qbase + ((4 * a + k) * 32 + lane) * 16);
-                    qa[k][0] = f.x;
-                    qa[k][1] = f.y;
-                    qa[k][2] = f.z;
-                    qa[k][3] = f.w;
-                }
+                for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int x = 0; x < NS; ++x)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint4 kw = ld_s128(kb + (4 * x + 2 * j) * D + 64 * a);
-                        const uint32_t wv[4] = {kw.x, kw.y, kw.z, kw.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t b0, b1;
-                            att_codes(wv[k], b0, b1);
-                            mma16816(s[x][j], qa[k], b0, b1);
+                    for (int z = 0; z < NR; ++z) {
+                        if (F::QS) {
+                            const uint2 f = ld_s64(qbase + (((4 * a + k) * NR + z) * 32 + lane) * 8);
+                            qa[k][z][0] = f.x;
+                            qa[k][z][1] = f.y;
+                        } else {
+                            qa[k][z][0] = qf[F::QS ? 0 : 4 * a + k][z][0];
+                            qa[k][z][1] = qf[F::QS ? 0 : 4 * a + k][z][1];
                         }
                     }
+#pragma unroll
+                for (int x = 0; x < NX; ++x) {
+                    // keys of tile rows g and g + 8
+                    const uint4 k0 = ld_s128(kb + 4 * x * D + 64 * a), k1 = ld_s128(kb + (4 * x + 2) * D + 64 * a);
+                    const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t f[4];
+                        att_codes(w0[k], f[0], f[2]);
+                        att_codes(w1[k], f[1], f[3]);
+#pragma unroll
+                        for (int z = 0; z < NR; ++z) {
+                            if (a == 0 && k == 0) mma16816_first(s[x][z], f, qa[k][z][0], qa[k][z][1]);
+                            else mma16816(s[x][z], f, qa[k][z][0], qa[k][z][1]);
+                        }
+                    }
+                }
             }
         }
 
         // ---- weights
-        const int j0 = cur_chunk(cc) * T, jt = j0 + TQ * t;
-        const bool whole = held && j0 + T <= q.len &&
-                           (!rowok || (p >= 0 && (j0 + T <= q.pre ||
-                                                  (j0 + T - 1 <= p && (P.window == 0 || p - j0 < P.window)))));
+        const int j0 = cur_chunk(cc) * T, jt = j0 + TQ * (g >> 1) + (g & 1);
+        bool whole = held;
+#pragma unroll
+        for (int z = 0; z < NR; ++z) whole = whole && (j0 + T <= vpre[z] || (j0 >= vlo[z] && j0 + T <= vhi[z]));
         const bool all_whole = __all_sync(0xFFFFFFFFu, whole);
         bool vzero;
-        const float rel = att_rel(vs * is, vzero), lv = log2f(rel);
-        const float f = qs * ks * (EXTRA ? 1.f : ATT_LOG2E);
-        float mx = -INFINITY;
+        const float rel = att_rel(vs * is, vzero), lv = att_lg2(rel);
+        uint32_t wb[NX][NR][2];
 #pragma unroll
-        for (int x = 0; x < NS; ++x)
+        for (int z = 0; z < NR; ++z) {
+            const float f = qs[z] * ks * (EXTRA ? 1.f : ATT_LOG2E);
+            float v[NX][2], mx = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int x = 0; x < NX; ++x)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float v = s[x][j][e] + s[x][j][2 + e];
-                    const int jj = jt + 4 * x + 2 * j + e;
+                    float y = s[x][z][2 * e] + s[x][z][2 * e + 1];
+                    const int j = jt + 4 * x + 2 * e;
                     if (EXTRA) {
-                        v *= f;
-                        if (P.softcap > 0.f) v = P.softcap * att_tanh(__fdividef(v, P.softcap));
-                        v -= slope * fabsf((float)(p - jj));
-                        v = fmaf(v, ATT_LOG2E, lv);
+                        y *= f;
+                        if (P.softcap > 0.f) y = P.softcap * att_tanh(__fdividef(y, P.softcap));
+                        y -= slope[z] * fabsf((float)(p[z] - j));
+                        y = fmaf(y, ATT_LOG2E, lv);
                     } else {
-                        v = fmaf(v, f, lv);
+                        y = fmaf(y, f, lv);
                     }
-                    if (!all_whole && rowok) {
-                        const bool see = att_sees(P, q, p, jj);
-                        if (see && !held) record_status(P.status, STATUS_BADARG);
-                        if (!see || !held) v = -INFINITY;
+                    if (!all_whole) {
+                        const bool see = j < vpre[z] || (j >= vlo[z] && j < vhi[z]);
+                        if (see && !held && vhi[z] != INT32_MAX) record_status(P.status, STATUS_BADARG);
+                        if (!see || !held) y = -INFINITY;
                     }
-                    s[x][j][e] = v;
-                    mx = fmaxf(mx, v);
+                    v[x][e] = y;
+                    mx = fmaxf(mx, y);
                 }
-        // no key of this thread seen: its page's scale, which may be NaN, does
-        // not count (a seen key of a NaN page still makes its weight NaN)
-        const float il = mx == -INFINITY ? 0.f : 1.f / rel;
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-        if (__any_sync(0xFFFFFFFFu, mx > m)) {
-            const float mn = fmaxf(m, mx), r = m == mn ? 1.f : att_ex2(m - mn);
-            m = mn;
-            l *= r;
+            // no key of this thread seen: its page's scale, which may be NaN,
+            // does not count (a seen key of a NaN page still makes its weight NaN)
+            const float il = mx == -INFINITY ? 0.f : att_rcp(rel);
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+            if (__any_sync(0xFFFFFFFFu, mx > m[z])) {
+                const float mn = fmaxf(m[z], mx), r = m[z] == mn ? 1.f : att_ex2(m[z] - mn);
+                m[z] = mn;
+                l[z] *= r;
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n)
+                for (int n = 0; n < D / 16; ++n)
 #pragma unroll
-                for (int z = 0; z < 4; ++z) o[n][z] *= r;
+                    for (int e = 0; e < 4; ++e) o[n][z][e] *= r;
+            }
+            const float ref = m[z] == -INFINITY ? 0.f : m[z] - ATT_SHIFT;
+            float sum = 0.f;
+#pragma unroll
+            for (int x = 0; x < NX; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float y = att_ex2(v[x][e] - ref);
+                    sum += y;
+                    wb[x][z][e] = split1(y);
+                }
+            l[z] = fmaf(sum, il, l[z]);
         }
-        const float ref = m == -INFINITY ? 0.f : m - ATT_SHIFT;
-        const uint32_t vmask = vzero ? 0u : 0xFFFFFFFFu;
-        uint32_t wa[NS][4];
+        if (__any_sync(0xFFFFFFFFu, vzero)) {
+            const uint32_t vmask = vzero ? 0u : 0xFFFFFFFFu;
 #pragma unroll
-        for (int x = 0; x < NS; ++x)
+            for (int x = 0; x < NX; ++x)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float w0 = att_ex2(s[x][j][0] - ref), w1 = att_ex2(s[x][j][1] - ref);
-                l = fmaf(w0 + w1, il, l);
-                att_split(w0, w1, wa[x][2 * j], wa[x][2 * j + 1]);
-                wa[x][2 * j] &= vmask;
-                wa[x][2 * j + 1] &= vmask;
+                for (int z = 0; z < NR; ++z) {
+                    wb[x][z][0] &= vmask;
+                    wb[x][z][1] &= vmask;
+                }
+        }
+#pragma unroll
+        for (int x = 0; x < NX; ++x)
+#pragma unroll
+            for (int z = 0; z < NR; ++z) {
+                wb[x][z][0] = transpose8(wb[x][z][0]);
+                wb[x][z][1] = transpose8(wb[x][z][1]);
             }
 
-        // ---- O += W V
+        // ---- O^T += V^T W^T
         const int hV = hK + 1;
         if (!arrived(hV)) return;
         issue(hV + NSLOT - 1);
         {
-            const uint32_t vb = wbase + (hV % NSLOT) * F::HBP + voff;
+            const uint32_t vb = wbase + cs * F::HBP + voff;
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-                uint32_t wv[4];
+            for (int n = 0; n < D / 16; ++n) {
+                uint32_t w0[4], w1[4];                    // dims 16 n + g and + 8
                 if (T == 64) {
-                    const uint4 z = ld_s128(vb + 8 * n * vw);
-                    wv[0] = z.x;
-                    wv[1] = z.y;
-                    wv[2] = z.z;
-                    wv[3] = z.w;
+                    const uint4 a = ld_s128(vb + 16 * n * vw), b = ld_s128(vb + (16 * n + 8) * vw);
+                    w0[0] = a.x;
+                    w0[1] = a.y;
+                    w0[2] = a.z;
+                    w0[3] = a.w;
+                    w1[0] = b.x;
+                    w1[1] = b.y;
+                    w1[2] = b.z;
+                    w1[3] = b.w;
                 } else {
-                    const uint2 z = ld_s64(vb + 8 * n * vw);
-                    wv[0] = z.x;
-                    wv[1] = z.y;
+                    const uint2 a = ld_s64(vb + 16 * n * vw), b = ld_s64(vb + (16 * n + 8) * vw);
+                    w0[0] = a.x;
+                    w0[1] = a.y;
+                    w1[0] = b.x;
+                    w1[1] = b.y;
                 }
 #pragma unroll
-                for (int x = 0; x < NS; ++x) {
-                    uint32_t b0, b1;
-                    att_codes(wv[x], b0, b1);
-                    mma16816(o[n], wa[x], b0, b1);
+                for (int x = 0; x < NX; ++x) {
+                    uint32_t f[4];
+                    att_codes(w0[x], f[0], f[2]);
+                    att_codes(w1[x], f[1], f[3]);
+#pragma unroll
+                    for (int z = 0; z < NR; ++z) mma16816(o[n][z], f, wb[x][z][0], wb[x][z][1]);
                 }
             }
         }
@@ -484,38 +572,35 @@ __global__ void __launch_bounds__(Dc<D>::NT, 1) kv8_decode_kernel(const AttnPara
         // ---- the tile, or this warp's stretch of it, ends
         const bool tile_end = cc.c == cc.d.nc - 1;
         if (tile_end || u == nu - 1) {
-            l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
-            l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
             const float up = att_pow2(e0);
-            if (tile_end && from_start) {
-                const float r = l == 0.f ? 0.f : up / l;
-                if (rowok) {
-                    float* y = P.out + qrow * P.ld_out + (int64_t)head * D + 2 * t;
-                    const bool vec = (reinterpret_cast<uintptr_t>(y) & 7) == 0;
 #pragma unroll
-                    for (int n = 0; n < D / 8; ++n) {
-                        const float a = (o[n][0] + o[n][2]) * r, b = (o[n][1] + o[n][3]) * r;
-                        if (vec) {
-                            *reinterpret_cast<float2*>(y + 8 * n) = make_float2(a, b);
-                        } else {
-                            y[8 * n] = a;
-                            y[8 * n + 1] = b;
-                        }
-                    }
+            for (int z = 0; z < NR; ++z) {
+                float sum = l[z];
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 4);
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
+                const int rt = cc.tile * RT + 4 * z + t;
+                if (rt >= q.n * grp) continue;
+                float* y;
+                float r;
+                if (tile_end && from_start) {
+                    y = P.out + (int64_t)(q.row0 + rt / grp) * P.ld_out + (int64_t)(cc.hk * grp + rt % grp) * D;
+                    r = sum == 0.f ? 0.f : up / sum;
+                } else {
+                    y = part + (2 * (int64_t)w + (from_start ? 1 : 0)) * part_floats(D);
+                    if (g == 0) *reinterpret_cast<float2*>(y + MAX_RT * D + 2 * (4 * z + t)) = make_float2(m[z], sum);
+                    y += (4 * z + t) * D;
+                    r = up;
                 }
-            } else {
-                float* y = part + (2 * (int64_t)w + (from_start ? 1 : 0)) * part_floats(D);
-                if (rowok) {
 #pragma unroll
-                    for (int n = 0; n < D / 8; ++n)
-                        *reinterpret_cast<float2*>(y + g * D + 8 * n + 2 * t) =
-                            make_float2((o[n][0] + o[n][2]) * up, (o[n][1] + o[n][3]) * up);
-                    if (t == 0) *reinterpret_cast<float2*>(y + 8 * D + 2 * g) = make_float2(m, l);
+                for (int n = 0; n < D / 16; ++n) {
+                    y[16 * n + g] = (o[n][z][0] + o[n][z][1]) * r;
+                    y[16 * n + 8 + g] = (o[n][z][2] + o[n][z][3]) * r;
                 }
             }
             fresh = true;
         }
-        if (u < nu - 1) cur_next<T>(P, cc);
+        if (u < nu - 1) cur_next<T, RT>(P, cc);
     }
 }
 
@@ -523,21 +608,21 @@ __global__ void __launch_bounds__(Dc<D>::NT, 1) kv8_decode_kernel(const AttnPara
 // several warps hold some, in the order of the line; zeros for rows that no
 // chunk reaches.
 constexpr int CMB_WARPS = 8;
-template <int D>
+template <int D, int NR>
 __global__ void __launch_bounds__(CMB_WARPS * 32) kv8_combine_kernel(const AttnParams P, int warps) {
-    constexpr int T = Dc<D>::T, V = D / 32;
+    constexpr int T = Dc<D, NR>::T, RT = Dc<D, NR>::RT, V = D / 32;
     __shared__ float acc[CMB_WARPS][D];
     __shared__ float red[CMB_WARPS][2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, head = blockIdx.x, tok = blockIdx.y + blockIdx.z * 65535;
     pdl_wait();
     if (tok >= P.s.ntok) return;
     const int s = kv_find(P.s.nseq, tok, [&](int i) { return kv_cu(P.s, i); });
-    const DecSeq d = dec_seq<T>(P, s);
+    const DecSeq d = dec_seq<T, RT>(P, s);
     if (tok >= d.q.row0 + d.q.n) return;
     const int64_t* base = reinterpret_cast<const int64_t*>(P.ws);
     const int64_t U = base[P.s.nseq];
     const int grp = P.n_q / P.c.n_kv, hk = head / grp;
-    const int r = (tok - d.q.row0) * grp + head % grp, tile = r >> 3, g = r & 7;
+    const int r = (tok - d.q.row0) * grp + head % grp, tile = r / RT, g = r % RT;
     float* y = P.out + (int64_t)tok * P.ld_out + (int64_t)head * D;
     if (d.nc == 0) {
         for (int i = threadIdx.x; i < D; i += CMB_WARPS * 32) y[i] = 0.f;
@@ -551,7 +636,7 @@ __global__ void __launch_bounds__(CMB_WARPS * 32) kv8_combine_kernel(const AttnP
     auto slot = [&](int k) { return part + (2 * (int64_t)k + (k == a ? 1 : 0)) * part_floats(D); };
     // the first warp's stretch begins with the tile; the later ones' at their first unit
     float m = -INFINITY;
-    for (int k = a + (int)threadIdx.x; k <= z; k += CMB_WARPS * 32) m = fmaxf(m, slot(k)[8 * D + 2 * g]);
+    for (int k = a + (int)threadIdx.x; k <= z; k += CMB_WARPS * 32) m = fmaxf(m, slot(k)[MAX_RT * D + 2 * g]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     if (lane == 0) red[warp][0] = m;
@@ -563,7 +648,7 @@ __global__ void __launch_bounds__(CMB_WARPS * 32) kv8_combine_kernel(const AttnP
 #pragma unroll 4
     for (int k = a + warp; k <= z; k += CMB_WARPS) {
         const float* x = slot(k);
-        const float2 ml = *reinterpret_cast<const float2*>(x + 8 * D + 2 * g);
+        const float2 ml = *reinterpret_cast<const float2*>(x + MAX_RT * D + 2 * g);
         const float c = ml.x == m ? 1.f : att_ex2(ml.x - m);
         l = fmaf(ml.y, c, l);
 #pragma unroll
@@ -586,15 +671,15 @@ __global__ void __launch_bounds__(CMB_WARPS * 32) kv8_combine_kernel(const AttnP
 
 constexpr int DEC_MAX_SMS = 160;
 
-template <int D>
+template <int D, int NR>
 cudaError_t decode_launch(const AttnParams& P, int sms, cudaStream_t st) {
-    using F = Dc<D>;
+    using F = Dc<D, NR>;
     // slices of T keys of a page's V rows, where a page holds more
     CUtensorMap vmap{};
     const int64_t pg = (int64_t)1 << P.c.pshift;
     if (pg > F::T && api_byte_map(&vmap, P.c.v, pg, D, P.c.n_pages * P.c.n_kv, F::T, D) != 0) return cudaErrorInvalidValue;
     const bool extra = P.softcap > 0.f || P.slopes;
-    auto kern = extra ? kv8_decode_kernel<D, true> : kv8_decode_kernel<D, false>;
+    auto kern = extra ? kv8_decode_kernel<D, NR, true> : kv8_decode_kernel<D, NR, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
     if (e != cudaSuccess) return e;
     const int grid = sms < DEC_MAX_SMS ? sms : DEC_MAX_SMS;
@@ -610,20 +695,28 @@ cudaError_t decode_launch(const AttnParams& P, int sms, cudaStream_t st) {
     at.val.programmaticStreamSerializationAllowed = 1;
     c.attrs = &at;
     c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, kv8_combine_kernel<D>, P, grid * F::NC);
+    return cudaLaunchKernelEx(&c, kv8_combine_kernel<D, NR>, P, grid * F::NC);
+}
+
+// Four rows per tile where a sequence's rows of a kv head are at most that on
+// average (the codes are then read and converted once), else eight.
+template <int D>
+cudaError_t decode_rows(const AttnParams& P, int sms, cudaStream_t st) {
+    return (int64_t)P.s.ntok * (P.n_q / P.c.n_kv) <= 4 * (int64_t)P.s.nseq ? decode_launch<D, 1>(P, sms, st)
+                                                                            : decode_launch<D, 2>(P, sms, st);
 }
 
 }  // namespace
 
 size_t kv8_attn_workspace(int n_q, int n_kv, int d, int nseq, int ntok) {
-    const int nw = d == 64 ? Dc<64>::NC : d == 128 ? Dc<128>::NC : Dc<256>::NC;
-    return base_bytes(nseq) + (size_t)DEC_MAX_SMS * nw * 2 * part_floats(d) * sizeof(float);
+    const int nc = d == 256 ? Dc<256, 1>::NC : Dc<128, 1>::NC;           // the most warps of a CTA
+    return base_bytes(nseq) + (size_t)DEC_MAX_SMS * nc * 2 * part_floats(d) * sizeof(float);
 }
 
 cudaError_t launch_kv8_attn(const AttnParams& P, int sms, cudaStream_t st) {
-    return P.c.d == 64    ? decode_launch<64>(P, sms, st)
-           : P.c.d == 128 ? decode_launch<128>(P, sms, st)
-                          : decode_launch<256>(P, sms, st);
+    return P.c.d == 64    ? decode_rows<64>(P, sms, st)
+           : P.c.d == 128 ? decode_rows<128>(P, sms, st)
+                          : decode_rows<256>(P, sms, st);
 }
 
 }  // namespace lq
