@@ -21,11 +21,17 @@
 // quarter of the SMs' issue slots, the rest of a chunk's work a fifth.
 //
 // Split.  (sequence, kv head, row tile, chunk) are numbered in one line and
-// dealt to the warps of one CTA per SM in equal shares, whatever the lengths;
-// they never meet.  A warp keeps a running maximum, sum and O for its stretch
-// of a tile; a tile that spans several warps leaves one partial result per
-// warp and kv8_combine_kernel joins them in order.  The shares depend on the
-// lengths and the SM count only, so results are reproducible.
+// dealt to the warps of one CTA per SM in equal shares, whatever the lengths.
+// A warp keeps a running maximum, sum and O for its stretch of a tile.  A
+// stretch that is not a whole tile leaves a partial result in shared memory;
+// at the end the CTA's first warp of a tile joins those of its warps, and of the
+// CTAs that share a tile the last to finish joins theirs from the workspace (a
+// counter per CTA, which a first small kernel clears while this one is being
+// launched).
+// Partials are joined in the order of the line whoever comes last, and the
+// shares depend on the lengths and the SM count only, so results are
+// reproducible.  (Joining in a second kernel cost 8 to 16 us.  The code here is
+// kept short: it runs once, from a cold instruction cache.)
 //
 // Loads.  Each warp streams its chunks through its own ring of half-chunks
 // (K, then V), always all but one of them in flight: bulk copies by its first
@@ -164,29 +170,52 @@ __device__ __forceinline__ void cur_next(const AttnParams& P, Cur& k) {
 }
 __device__ __forceinline__ int cur_chunk(const Cur& k) { return k.c < k.d.na ? k.c : k.d.cb + (k.c - k.d.na); }
 
-// Workspace: base [nseq + 1] int64 (padded), then the partial results:
-// 2 per worker, [MAX_RT rows][D] of O, then [MAX_RT][2] of (max, sum).
+// Workspace: a counter per CTA, then the partial results: 2 per worker (of
+// the tile that its share begins in, and of the one that it ends in),
+// [MAX_RT rows][D] of O, then [MAX_RT][2] of (max, sum).
+constexpr int DEC_MAX_SMS = 160;
+constexpr size_t COUNT_BYTES = 1024;
 __host__ __device__ constexpr int64_t part_floats(int d) { return MAX_RT * (int64_t)d + 2 * MAX_RT; }
-__host__ __device__ inline size_t base_bytes(int nseq) { return ((size_t)(nseq + 1) * 8 + 255) & ~size_t(255); }
 
 // First worker of W whose share [U w / W, U (w + 1) / W) holds unit u.
 __device__ __forceinline__ int owner(int64_t u, int64_t U, int W) { return (int)(((u + 1) * W - 1) / U); }
 
+// A partial result: its tile's units [b0, b0 + nc) and rows.
+struct Stretch {
+    int64_t b0;
+    int32_t nc, row0, hk, r0, rows;
+};
+
+__global__ void kv8_clear_kernel(int* count) {
+    pdl_launch_dependents();
+    count[threadIdx.x] = 0;
+}
+
 template <int D, int NR, bool EXTRA>
-__global__ void __launch_bounds__(Dc<D, NR>::NT, 1) kv8_decode_kernel(const AttnParams P, const __grid_constant__ CUtensorMap vmap) {
+__global__ void __launch_bounds__(Dc<D, NR>::NT, 1) kv8_decode_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ CUtensorMap vmap) {
     using F = Dc<D, NR>;
     constexpr int T = F::T, TQ = F::TQ, NX = F::NX, NT = F::NT, NC = F::NC, NSLOT = F::NSLOT, RT = F::RT;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t tb[NT];
     __shared__ int64_t wsum[NC];
     __shared__ uint64_t full[NC][NSLOT];
+    __shared__ Stretch parts[NC][2];                      // the partials that a warp left, and how many
+    __shared__ int nparts[NC];
+    __shared__ int64_t first[NC + 1];                     // a warp's first unit; behind the last one's
+    // what the end needs, out of the main loop's registers: the units in all,
+    // warps in use per CTA, before this CTA, in this CTA
+    __shared__ struct {
+        int64_t units;
+        int wpc, w0, act;
+    } line;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    pdl_launch_dependents();
+    const int grp = P.n_q / P.c.n_kv;
     if (tid < NC * NSLOT) {
         // an arrival for each page of a chunk
         mbar_init(&full[0][0] + tid, P.c.pshift == 4 ? T / 16 : P.c.pshift == 5 ? T / 32 : max(1, T >> P.c.pshift));
         fence_mbar_init();
     }
+    pdl_wait();
 
     // ---- the line: thread i sums the units of its sequences
     const int per = (P.s.nseq + NT - 1) / NT;
@@ -206,24 +235,36 @@ __global__ void __launch_bounds__(Dc<D, NR>::NT, 1) kv8_decode_kernel(const Attn
         U += wsum[i];
     }
     tb[tid] = before + inc - mine;
-    if (blockIdx.x == 0) {
-        int64_t* base = reinterpret_cast<int64_t*>(P.ws);
-        int64_t b = before + inc - mine;
-        for (int s = tid * per; s < min((tid + 1) * per, P.s.nseq); ++s) {
-            base[s] = b;
-            b += dec_units(P, dec_seq<T, RT>(P, s));
-        }
-        if (tid == 0) base[P.s.nseq] = U;
-    }
     __syncthreads();
 
-    // warps in use (none without a unit) and this one: few units go to different SMs
-    const int W = (int)min((int64_t)gridDim.x * NC, U), w = warp * gridDim.x + blockIdx.x;
-    if (w >= W) return;                                   // warps never meet again
-    const int64_t u0 = U * w / W;
-    const int nu = (int)(U * (w + 1) / W - u0);
+    // rows of sequences without keys
+    for (int s = blockIdx.x; s < P.s.nseq; s += gridDim.x) {
+        const DecSeq d = dec_seq<T, RT>(P, s);
+        if (d.nc > 0) continue;
+        const int wd = P.n_q * D;
+        for (int64_t i = tid; i < (int64_t)d.q.n * wd; i += NT) P.out[(d.q.row0 + i / wd) * P.ld_out + i % wd] = 0.f;
+    }
+
+    // warps in use, per CTA and in all (none without a unit)
+    {
+        const int wpc = (int)min((int64_t)NC, (U + gridDim.x - 1) / gridDim.x);
+        const int W = (int)min((int64_t)gridDim.x * wpc, U), w0 = blockIdx.x * wpc, act = min(wpc, W - w0);
+        if (act <= 0) return;                             // (the whole CTA)
+        if (tid <= act) first[tid] = U * (w0 + tid) / W;
+        if (tid == 0) {
+            line.units = U;
+            line.wpc = wpc;
+            line.w0 = w0;
+            line.act = act;
+        }
+    }
+    if (lane == 0) nparts[warp] = 0;
+    __syncthreads();
+    if (warp < *(volatile int*)&line.act) {
+    const int nu = (int)(first[warp + 1] - first[warp]);
     Cur cc;                                               // the unit at hand
     {
+        const int64_t u0 = first[warp];
         const int i = kv_find(NT, u0, [&](int x) { return tb[x]; });
         int64_t b = tb[i];
         int s = i * per;
@@ -296,8 +337,6 @@ __global__ void __launch_bounds__(Dc<D, NR>::NT, 1) kv8_decode_kernel(const Attn
     };
     for (int h = 0; h < NSLOT - 1; ++h) issue(h);
 
-    const int grp = P.n_q / P.c.n_kv;
-    float* part = reinterpret_cast<float*>(P.ws + base_bytes(P.s.nseq));
     const int vw = min(Pg, T);                            // keys per row of V in shared memory
     const uint32_t voff = (uint32_t)(TQ * t / vw) * ((uint32_t)vw * D + vpad) + (TQ * t) % vw + g * vw;
     const uint32_t koff = (TQ * (g >> 1) + (g & 1)) * D + 16 * t, moff = (uint32_t)(TQ * (g >> 1) >> lpw) * 4;
@@ -307,7 +346,7 @@ __global__ void __launch_bounds__(Dc<D, NR>::NT, 1) kv8_decode_kernel(const Attn
     // slope, position, and the keys it sees, [vlo, vhi) and [0, vpre)
     float m[NR], l[NR], qs[NR], slope[NR];
     int p[NR], vlo[NR], vhi[NR], vpre[NR];
-    int e0 = 0;
+    int e0 = 0, np = 0;                                   // (np: partials left)
     float is = 1.f;                                       // 2^-e0
     bool fresh = true, from_start = false;
 
@@ -408,7 +447,7 @@ __global__ void __launch_bounds__(Dc<D, NR>::NT, 1) kv8_decode_kernel(const Attn
 
         // ---- S^T = K Q^T
         const int hK = 2 * u;
-        if (!arrived(hK)) return;
+        if (!arrived(hK)) break;
         issue(hK + NSLOT - 1);
         const uint32_t mt = mbase + (u % F::NMETA) * 32 + moff;
         const float ks = ld_sf(mt), vs = ld_sf(mt + 16);
@@ -534,7 +573,7 @@ __global__ void __launch_bounds__(Dc<D, NR>::NT, 1) kv8_decode_kernel(const Attn
 
         // ---- O^T += V^T W^T
         const int hV = hK + 1;
-        if (!arrived(hV)) return;
+        if (!arrived(hV)) break;
         issue(hV + NSLOT - 1);
         {
             const uint32_t vb = wbase + cs * F::HBP + voff;
@@ -573,6 +612,15 @@ __global__ void __launch_bounds__(Dc<D, NR>::NT, 1) kv8_decode_kernel(const Attn
         const bool tile_end = cc.c == cc.d.nc - 1;
         if (tile_end || u == nu - 1) {
             const float up = att_pow2(e0);
+            const bool whole_tile = tile_end && from_start;
+            // a partial goes to this warp's ring if that is done with, unless
+            // the CTA has no other of the tile
+            const int64_t b0 = first[warp] + u - cc.c, b1 = b0 + cc.d.nc;
+            const int act = *(volatile int*)&line.act, w0 = *(volatile int*)&line.w0;
+            const bool alone = (warp == 0 || b0 >= first[warp]) && (warp == act - 1 || b1 <= first[warp + 1]);
+            float* const mine = !alone && u == nu - 1
+                                    ? reinterpret_cast<float*>(smem + warp * F::WB)
+                                    : reinterpret_cast<float*>(P.ws + COUNT_BYTES) + (2 * (int64_t)(w0 + warp) + (from_start ? 1 : 0)) * part_floats(D);
 #pragma unroll
             for (int z = 0; z < NR; ++z) {
                 float sum = l[z];
@@ -583,11 +631,11 @@ __global__ void __launch_bounds__(Dc<D, NR>::NT, 1) kv8_decode_kernel(const Attn
                 if (rt >= q.n * grp) continue;
                 float* y;
                 float r;
-                if (tile_end && from_start) {
+                if (whole_tile) {
                     y = P.out + (int64_t)(q.row0 + rt / grp) * P.ld_out + (int64_t)(cc.hk * grp + rt % grp) * D;
                     r = sum == 0.f ? 0.f : up / sum;
                 } else {
-                    y = part + (2 * (int64_t)w + (from_start ? 1 : 0)) * part_floats(D);
+                    y = mine;
                     if (g == 0) *reinterpret_cast<float2*>(y + MAX_RT * D + 2 * (4 * z + t)) = make_float2(m[z], sum);
                     y += (4 * z + t) * D;
                     r = up;
@@ -599,77 +647,150 @@ __global__ void __launch_bounds__(Dc<D, NR>::NT, 1) kv8_decode_kernel(const Attn
                 }
             }
             fresh = true;
+            if (!whole_tile) {
+                if (lane == 0) parts[warp][np] = Stretch{b0, cc.d.nc, q.row0, cc.hk, cc.tile * RT, min(RT, q.n * grp - cc.tile * RT)};
+                ++np;
+            }
         }
         if (u < nu - 1) cur_next<T, RT>(P, cc);
     }
-}
 
-// Block (head, token): joins the partial results of one query row where
-// several warps hold some, in the order of the line; zeros for rows that no
-// chunk reaches.
-constexpr int CMB_WARPS = 8;
-template <int D, int NR>
-__global__ void __launch_bounds__(CMB_WARPS * 32) kv8_combine_kernel(const AttnParams P, int warps) {
-    constexpr int T = Dc<D, NR>::T, RT = Dc<D, NR>::RT, V = D / 32;
-    __shared__ float acc[CMB_WARPS][D];
-    __shared__ float red[CMB_WARPS][2];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, head = blockIdx.x, tok = blockIdx.y + blockIdx.z * 65535;
-    pdl_wait();
-    if (tok >= P.s.ntok) return;
-    const int s = kv_find(P.s.nseq, tok, [&](int i) { return kv_cu(P.s, i); });
-    const DecSeq d = dec_seq<T, RT>(P, s);
-    if (tok >= d.q.row0 + d.q.n) return;
-    const int64_t* base = reinterpret_cast<const int64_t*>(P.ws);
-    const int64_t U = base[P.s.nseq];
-    const int grp = P.n_q / P.c.n_kv, hk = head / grp;
-    const int r = (tok - d.q.row0) * grp + head % grp, tile = r / RT, g = r % RT;
-    float* y = P.out + (int64_t)tok * P.ld_out + (int64_t)head * D;
-    if (d.nc == 0) {
-        for (int i = threadIdx.x; i < D; i += CMB_WARPS * 32) y[i] = 0.f;
-        return;
+    if (lane == 0) nparts[warp] = np;
     }
-    const int64_t b = base[s] + ((int64_t)hk * d.tiles + tile) * d.nc;
-    const int W = (int)min((int64_t)warps, U);
-    const int a = owner(b, U, W), z = owner(b + d.nc - 1, U, W);
-    if (a == z) return;                                   // that warp wrote the row
-    const float* part = reinterpret_cast<const float*>(P.ws + base_bytes(P.s.nseq));
-    auto slot = [&](int k) { return part + (2 * (int64_t)k + (k == a ? 1 : 0)) * part_floats(D); };
-    // the first warp's stretch begins with the tile; the later ones' at their first unit
-    float m = -INFINITY;
-    for (int k = a + (int)threadIdx.x; k <= z; k += CMB_WARPS * 32) m = fmaxf(m, slot(k)[MAX_RT * D + 2 * g]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    if (lane == 0) red[warp][0] = m;
+
+    // ---- join the partials of the CTA's warps, then those of the CTAs: each
+    // warp the tiles whose first part in this CTA is its own
     __syncthreads();
-    for (int i = 0; i < CMB_WARPS; ++i) m = fmaxf(m, red[i][0]);
-    float l = 0.f, o[V];
+    const int64_t units = *(volatile int64_t*)&line.units;
+    const int wpc = *(volatile int*)&line.wpc, w0 = *(volatile int*)&line.w0, act = *(volatile int*)&line.act;
+    float* const part = reinterpret_cast<float*>(P.ws + COUNT_BYTES);
+    constexpr int64_t PF = part_floats(D);
+#pragma unroll 1
+    for (int i = 0; i < nparts[warp]; ++i) {
+        const Stretch s = parts[warp][i];
+        const bool starts = s.b0 >= first[warp];
+        if (!starts && warp > 0) continue;
+        const int64_t b1 = s.b0 + s.nc;
+        int e = warp;
+        while (e + 1 < act && first[e + 1] < b1) ++e;     // the last warp of the tile in this CTA
+        const bool inside = starts && b1 <= first[act];
+        // the tile's first worker, and the CTAs
+        const int W = (int)min((int64_t)gridDim.x * wpc, units);
+        const int a = starts ? w0 + warp : owner(s.b0, units, W), ca = a / wpc;
+        const int cb = inside ? ca : owner(b1 - 1, units, W) / wpc;
+        float* const own = part + (2 * (int64_t)(w0 + warp) + (starts ? 1 : 0)) * PF;
+#pragma unroll 1
+        for (int stage = 0; stage < 2; ++stage) {
+            const int n = stage ? cb - ca + 1 : e - warp + 1;
+            if (stage == 0 && n == 1) continue;           // already in the workspace
+            if (stage == 1) {
+                if (inside) break;
+                __threadfence();                          // the CTA's partial is out before it is counted
+                __syncwarp();
+                int k = 0;
+                if (lane == 0) k = atomicAdd(reinterpret_cast<int*>(P.ws) + ca, 1);
+                if (__shfl_sync(0xFFFFFFFFu, k, 0) != n - 1) break;
+                __threadfence();
+            }
+            // lane x: where partial k0 + x lies, its maxima, its weights
+            constexpr int V4 = RT * D / 128;              // float4 of a partial per lane
+            float4 acc[V4];
+            float M[RT], l[RT];
 #pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = 0.f;
-#pragma unroll 4
-    for (int k = a + warp; k <= z; k += CMB_WARPS) {
-        const float* x = slot(k);
-        const float2 ml = *reinterpret_cast<const float2*>(x + MAX_RT * D + 2 * g);
-        const float c = ml.x == m ? 1.f : att_ex2(ml.x - m);
-        l = fmaf(ml.y, c, l);
+            for (int v = 0; v < V4; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = fmaf(x[g * D + lane + 32 * e], c, o[e]);
-    }
+            for (int r = 0; r < RT; ++r) {
+                M[r] = -INFINITY;
+                l[r] = 0.f;
+            }
+#pragma unroll 1
+            for (int k0 = 0; k0 < n; k0 += 32) {
+                const int k = min(k0 + lane, n - 1);
+                const float* x;
+                if (stage) {
+                    const int y = max(a, (ca + k) * wpc);
+                    x = part + (2 * (int64_t)y + (y == a)) * PF;
+                } else {
+                    // (the last warp may have gone on with another tile: its ring was not free then)
+                    x = warp + k < e || b1 >= first[e + 1] ? reinterpret_cast<const float*>(smem + (warp + k) * F::WB)
+                                                           : part + 2 * (int64_t)(w0 + e) * PF;
+                }
+                float c[RT];
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[warp][lane + 32 * e] = o[e];
-    if (lane == 0) red[warp][1] = l;
-    __syncthreads();
-    l = 0.f;
-    for (int i = 0; i < CMB_WARPS; ++i) l += red[i][1];
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int i = threadIdx.x; i < D; i += CMB_WARPS * 32) {
-        float v = 0.f;
+                for (int r = 0; r < RT; ++r) {
+                    const float mk = k0 + lane < n ? x[MAX_RT * D + 2 * r] : -INFINITY;
+                    const float lk = k0 + lane < n ? x[MAX_RT * D + 2 * r + 1] : 0.f;
+                    float mx = fmaxf(mk, M[r]);
 #pragma unroll
-        for (int k = 0; k < CMB_WARPS; ++k) v += acc[k][i];
-        y[i] = v * inv;
+                    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+                    const float f = M[r] == mx ? 1.f : att_ex2(M[r] - mx);
+                    M[r] = mx;
+                    c[r] = k0 + lane >= n ? 0.f : mk == mx ? 1.f : att_ex2(mk - mx);
+                    l[r] = fmaf(lk, c[r], l[r] * f);
+#pragma unroll
+                    for (int v = 0; v < V4; ++v)
+                        if (128 * v / D <= r && r <= (128 * v + 127) / D && (D >= 128 || (lane >> 4) == (r & 1))) {
+                            acc[v].x *= f;
+                            acc[v].y *= f;
+                            acc[v].z *= f;
+                            acc[v].w *= f;
+                        }
+                }
+                const int m = min(32, n - k0);
+                constexpr int KB = V4 >= 16 ? 1 : V4 >= 8 ? 2 : 4;          // partials at a time: their loads first
+#pragma unroll 1
+                for (int kk = 0; kk < m; kk += KB) {
+                    float4 z[KB][V4];
+#pragma unroll
+                    for (int b = 0; b < KB; ++b) {
+                        const float4* y = reinterpret_cast<const float4*>(
+                            __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(x), min(kk + b, m - 1))) + lane;
+#pragma unroll
+                        for (int v = 0; v < V4; ++v) z[b][v] = y[32 * v];
+                    }
+#pragma unroll
+                    for (int b = 0; b < KB; ++b)
+#pragma unroll
+                        for (int r = 0; r < RT; ++r) {
+                            float ck = __shfl_sync(0xFFFFFFFFu, c[r], min(kk + b, m - 1));
+                            if (kk + b >= m || r >= s.rows) ck = 0.f;
+#pragma unroll
+                            for (int v = 0; v < V4; ++v)
+                                if (128 * v / D <= r && r <= (128 * v + 127) / D && (D >= 128 || (lane >> 4) == (r & 1))) {
+                                    acc[v].x = fmaf(z[b][v].x, ck, acc[v].x);
+                                    acc[v].y = fmaf(z[b][v].y, ck, acc[v].y);
+                                    acc[v].z = fmaf(z[b][v].z, ck, acc[v].z);
+                                    acc[v].w = fmaf(z[b][v].w, ck, acc[v].w);
+                                }
+                        }
+                }
+            }
+            const bool final = stage == 1 || inside;
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], o);
+                if (r >= s.rows) continue;
+                const int rt = s.r0 + r;
+                float* y = final ? P.out + (int64_t)(s.row0 + rt / grp) * P.ld_out + (int64_t)(s.hk * grp + rt % grp) * D : own + r * D;
+                const float f = !final ? 1.f : l[r] == 0.f ? 0.f : 1.f / l[r];
+#pragma unroll
+                for (int v = 0; v < V4; ++v)
+                    if (128 * v / D <= r && r <= (128 * v + 127) / D && (D >= 128 || (lane >> 4) == (r & 1))) {
+                        const int d = (128 * v + 4 * lane) % D;
+                        y[d] = acc[v].x * f;
+                        y[d + 1] = acc[v].y * f;
+                        y[d + 2] = acc[v].z * f;
+                        y[d + 3] = acc[v].w * f;
+                    }
+                if (!final && lane == 0) {
+                    own[MAX_RT * D + 2 * r] = M[r];
+                    own[MAX_RT * D + 2 * r + 1] = l[r];
+                }
+            }
+        }
     }
 }
-
-constexpr int DEC_MAX_SMS = 160;
 
 template <int D, int NR>
 cudaError_t decode_launch(const AttnParams& P, int sms, cudaStream_t st) {
@@ -683,19 +804,19 @@ cudaError_t decode_launch(const AttnParams& P, int sms, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
     if (e != cudaSuccess) return e;
     const int grid = sms < DEC_MAX_SMS ? sms : DEC_MAX_SMS;
-    kern<<<grid, F::NT, F::SMEM, st>>>(P, vmap);
+    kv8_clear_kernel<<<1, DEC_MAX_SMS, 0, st>>>(reinterpret_cast<int*>(P.ws));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t c{};
-    const int ty = P.s.ntok < 65535 ? P.s.ntok : 65535;
-    c.gridDim = dim3((unsigned)P.n_q, (unsigned)ty, (unsigned)((P.s.ntok + 65534) / 65535));
-    c.blockDim = dim3(CMB_WARPS * 32);
+    c.gridDim = dim3((unsigned)grid);
+    c.blockDim = dim3(F::NT);
+    c.dynamicSmemBytes = F::SMEM;
     c.stream = st;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     c.attrs = &at;
     c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, kv8_combine_kernel<D, NR>, P, grid * F::NC);
+    return cudaLaunchKernelEx(&c, kern, P, vmap);
 }
 
 // Four rows per tile where a sequence's rows of a kv head are at most that on
@@ -710,7 +831,7 @@ cudaError_t decode_rows(const AttnParams& P, int sms, cudaStream_t st) {
 
 size_t kv8_attn_workspace(int n_q, int n_kv, int d, int nseq, int ntok) {
     const int nc = d == 256 ? Dc<256, 1>::NC : Dc<128, 1>::NC;           // the most warps of a CTA
-    return base_bytes(nseq) + (size_t)DEC_MAX_SMS * nc * 2 * part_floats(d) * sizeof(float);
+    return COUNT_BYTES + (size_t)DEC_MAX_SMS * nc * 2 * part_floats(d) * sizeof(float);
 }
 
 cudaError_t launch_kv8_attn(const AttnParams& P, int sms, cudaStream_t st) {
