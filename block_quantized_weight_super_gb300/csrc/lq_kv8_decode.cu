@@ -49,12 +49,12 @@ struct Dc {
     static constexpr int TQ = T / 4;                         // keys of a quad pair
     static constexpr int NX = T / 16;                        // 16-key MMA tiles of a chunk
     // warps: 2 to 4 per scheduler, as registers allow
-    static constexpr int NC = NR == 1 ? (D == 256 ? 10 : 16) : (D == 256 ? 8 : 12);
+    static constexpr int NC = D == 256 ? 8 : NR == 1 ? 16 : 12;
     static constexpr int NT = NC * 32;
     static constexpr int NSLOT = D == 256 ? 2 : 3;           // half-chunks of a warp's ring
     static constexpr int HB = T * D;                         // bytes of a half-chunk
     static constexpr int HBP = HB + 128;                     // with the padding between pages of V
-    static constexpr bool QS = D == 256;                    // q fragments in shared memory (registers are full)
+    static constexpr bool QS = D == 256 && NR == 2;          // q fragments in shared memory (registers are full)
     static constexpr int QB = QS ? D * 16 * NR : 0;
     static constexpr int NMETA = 4;                          // chunks whose scales are held
     static constexpr int WB = NSLOT * HBP + QB + NMETA * 32; // shared memory of a warp (a multiple of 128)
@@ -827,6 +827,8 @@ cudaError_t decode_rows(const AttnParams& P, int sms, cudaStream_t st) {
                                                                             : decode_launch<D, 2>(P, sms, st);
 }
 
+constexpr int64_t PREFILL_MIN_ROWS = 64;
+
 }  // namespace
 
 size_t kv8_attn_workspace(int n_q, int n_kv, int d, int nseq, int ntok) {
@@ -834,7 +836,10 @@ size_t kv8_attn_workspace(int n_q, int n_kv, int d, int nseq, int ntok) {
     return COUNT_BYTES + (size_t)DEC_MAX_SMS * nc * 2 * part_floats(d) * sizeof(float);
 }
 
+// Many rows per sequence and kv head: the prefill kernel, whose tiles hold
+// 128 rows and are worth filling by half.
 cudaError_t launch_kv8_attn(const AttnParams& P, int sms, cudaStream_t st) {
+    if ((int64_t)P.s.ntok * (P.n_q / P.c.n_kv) >= PREFILL_MIN_ROWS * (int64_t)P.s.nseq) return launch_kv8_prefill(P, st);
     return P.c.d == 64    ? decode_rows<64>(P, sms, st)
            : P.c.d == 128 ? decode_rows<128>(P, sms, st)
                           : decode_rows<256>(P, sms, st);

@@ -1,0 +1,555 @@
+// lq_kv8_prefill.cu -- attention over the 8-bit paged cache for many query rows
+// per sequence (prompts): a contraction, on the fifth-generation tensor cores.
+//
+// A CTA takes 128 query rows of one kv head (tokens x the heads of its group,
+// so the codes of a kv head are converted once for the whole group) and walks
+// the keys that any of them sees in tiles of NK.  fp32 accuracy: the rows as
+// fp16 hi and lo pieces (scaled to a power of two per row), the softmax
+// weights likewise, the codes exact in fp16; so each product is two MMAs and
+// half the fp16 rate is the ceiling.
+//   S = Q K^T   A = the pieces of Q in tensor memory (written once), B = the K
+//               tile in shared memory; NK columns of fp32, two buffers;
+//   O += W V    A = the weights' pieces in tensor memory, written over the S
+//               they came from; B = the V tile (tokens adjacent, as the pages
+//               hold it); D columns of fp32.
+// With both A operands in tensor memory an MMA of 64 cycles reads 4 KB of
+// shared memory; from shared memory it would read 8 KB, the port's limit.
+// (D = 256 has no room there for the lo pieces of Q: those stay in shared
+// memory.)
+//
+// Softmax.  Thread r of warps 0-3 owns row r (tensor-memory lane r).  A first
+// pass over S finds the tile's maximum, a second one forms the weights and
+// writes their pieces.  The scales of a page enter as one factor and one
+// summand per 16 keys: weight = 2^(S qs ks + log2(vs / 2^e0) - ref), so V is
+// used as codes; the row sum divides the value scale out again per 16 keys.
+// ref is the row's maximum when it was last set; it is raised, and O rescaled,
+// only when a tile exceeds it by 2^4, so O is rarely touched.
+//
+// Warps.  0-3 softmax (one per scheduler), 4-11 converters: each takes the
+// codes of 16 keys (one page) of a tile from global memory through registers,
+// a tile ahead, into fp16 in the MMA's core-matrix layout; 12 issues the MMAs.
+// Tensor order: PV(j), S(j + 2), PV(j + 1), ...: while PV(j) and S(j + 2) run the
+// softmax works on tile j + 1.
+//
+// Every wait is bounded: on a timeout a role records it and leaves its loop;
+// the MMAs in flight end (bounded) before the tensor memory is freed.
+#include "lq_kv8_attn.cuh"
+
+namespace lq {
+namespace {
+
+constexpr int PF_ROWS = 128;
+constexpr int PF_CONV = 8;                                   // converter warps
+constexpr int PF_THREADS = (4 + PF_CONV + 1) * 32;
+constexpr int PF_MMA_WARP = 4 + PF_CONV;
+// Weights are 2^(u - ref + 11), at most 2^15: the lo pieces' floor of 2^-25 is
+// 2^-36 of the row's largest weight or less.
+constexpr float PF_SHIFT = 11.f;
+constexpr float PF_RAISE = 4.f;
+
+template <int D>
+struct Pf {
+    static constexpr int NK = D == 256 ? 64 : 128;           // keys of a tile
+    static constexpr int NG = NK / 16;                       // 16-key groups
+    static constexpr int WPG = PF_CONV / NG;                 // converter warps of a group
+    static constexpr bool QLO_SMEM = D == 256;
+    static constexpr uint32_t KB = NK * D * 2;               // bytes of a K or V tile
+    static constexpr uint32_t K_OFF = 0, V_OFF = 2 * KB, Q_OFF = 4 * KB;
+    static constexpr uint32_t META_OFF = Q_OFF + (QLO_SMEM ? PF_ROWS * D * 2 : 0);
+    // (ks, log2, 1 / rel) of the groups of 4 tiles; and one CTA per SM, as each takes all of the tensor memory
+    static constexpr uint32_t SMEM = META_OFF + 4 * NG * 16 > 120 * 1024 ? META_OFF + 4 * NG * 16 : 120 * 1024;
+    // tensor memory columns
+    static constexpr uint32_t T_S = 0, T_O = 2 * NK, T_QH = T_O + D, T_QL = T_QH + D / 2;
+    static_assert(T_QH + (QLO_SMEM ? D / 2 : D) <= 512, "tensor memory");
+    static constexpr uint32_t SBO_K = 16 * D, SBO_V = 16 * NK;    // core matrices of 8 rows; 128 bytes along K
+};
+
+__device__ __forceinline__ uint64_t pf_desc(uint32_t addr, uint32_t sbo) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)(128 >> 4) << 16 | (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 |
+           (uint64_t)1 << 46;                                // no swizzle, this architecture's descriptor version
+}
+__host__ __device__ constexpr uint32_t pf_idesc(int n) {     // fp16 A and B, K-major, fp32 accumulators, M = 128
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ void pf_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void pf_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void pf_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void t_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void t_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void t_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+#define LQ_R8(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), "=r"(x[i + 4]), "=r"(x[i + 5]), "=r"(x[i + 6]), "=r"(x[i + 7])
+#define LQ_S8(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]), "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
+// The load and its wait in one statement: uses of v could otherwise be moved
+// between them.
+__device__ __forceinline__ void t_ld32(uint32_t a, uint32_t (&v)[32]) {
+    asm volatile(
+        "{\n\ttcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n\t}"
+        : LQ_R8(v, 0), LQ_R8(v, 8), LQ_R8(v, 16), LQ_R8(v, 24)
+        : "r"(a)
+        : "memory");
+}
+__device__ __forceinline__ void t_st32(uint32_t a, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(a),
+        LQ_S8(v, 0), LQ_S8(v, 8), LQ_S8(v, 16), LQ_S8(v, 24)
+        : "memory");
+}
+__device__ __forceinline__ void t_st16(uint32_t a, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(a),
+        LQ_S8(v, 0), LQ_S8(v, 8)
+        : "memory");
+}
+#undef LQ_R8
+#undef LQ_S8
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ float4 lds4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+    return v;
+}
+
+// Lane 0 waits (32 lanes polling one barrier serialise on it), the warp follows.
+__device__ __forceinline__ bool pf_wait(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait_bounded(bar, parity, timeout_ns);
+    __syncwarp();
+    return __shfl_sync(0xFFFFFFFFu, ok, 0);
+}
+
+template <int D, bool EXTRA>
+__global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid_constant__ AttnParams P) {
+    using F = Pf<D>;
+    constexpr int NK = F::NK, NG = F::NG;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], pv_done, q_full;
+    __shared__ uint32_t tslot;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int grp = P.n_q / P.c.n_kv, hk = blockIdx.y;
+
+    // ---- which rows: sequence s owns tiles from floor(cu[s] grp / 128) + s on;
+    // the last ones, which see the most keys, first
+    const int64_t x = (int64_t)gridDim.x - 1 - blockIdx.x;
+    auto base = [&](int i) { return (((int64_t)kv_cu(P.s, i) * grp) >> 7) + i; };
+    const int s = kv_find(P.s.nseq, x, base);
+    const AttSeq q = att_seq(P, s);
+    const int64_t rt0 = (x - base(s)) * PF_ROWS;               // the tile's first row of the sequence's rows
+    const int64_t nrows = (int64_t)q.n * grp;
+    if (rt0 >= nrows) return;
+    const int rows = (int)min((int64_t)PF_ROWS, nrows - rt0);
+    const int i0 = (int)(rt0 / grp), i1 = (int)((rt0 + rows - 1) / grp);
+    const int64_t p0 = max(q.start + i0, (int64_t)0), p1 = q.start + i1;    // positions of the rows that see anything
+    // key tiles: [0, na) and from cb on, nt in all
+    const int hi = p1 < 0 ? 0 : (int)min((int64_t)q.len, max(p1 + 1, (int64_t)q.pre));
+    const int lo = P.window ? (int)min(max(p0 - P.window + 1, (int64_t)0), (int64_t)hi) : 0;
+    const int ce = (hi + NK - 1) / NK, cb = min(lo / NK, ce), na = min((q.pre + NK - 1) / NK, cb);
+    const int nt = na + ce - cb;
+    auto key0 = [&](int j) { return (j < na ? j : cb + (j - na)) * NK; };
+    if (nt == 0) {
+        for (int64_t i = tid; i < (int64_t)rows * D; i += PF_THREADS) {
+            const int64_t r = rt0 + i / D;
+            P.out[(q.row0 + r / grp) * P.ld_out + (hk * grp + r % grp) * D + i % D] = 0.f;
+        }
+        return;
+    }
+    // the reference of the value scales
+    const int pe = att_page(P, s, key0(0));
+    const int e0 = pe >= 0 ? att_e0(__ldg(P.c.vs + (int64_t)pe * P.c.n_kv + hk)) : 0;
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&k_full[i], PF_CONV);
+            mbar_init(&v_full[i], PF_CONV);
+            mbar_init(&k_free[i], 1);
+            mbar_init(&v_free[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+        }
+        mbar_init(&pv_done, 1);
+        mbar_init(&q_full, 4);
+        fence_mbar_init();
+    }
+    if (warp == PF_MMA_WARP) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tslot)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    t_before();
+    __syncthreads();
+    t_after();
+    const uint32_t tmem = tslot, sbase = smem_u32(smem), meta = sbase + F::META_OFF;
+    bool ok = true;
+
+    if (warp < 4) {
+        // ---- softmax: thread = row
+        const int r = warp * 32 + lane;
+        const bool rok = r < rows;
+        const int64_t rr = rt0 + (rok ? r : 0);
+        const int head = hk * grp + (int)(rr % grp);
+        const int64_t qrow = q.row0 + rr / grp;
+        const int64_t pl = q.start + rr / grp;
+        const int p = (int)min(max(pl, (int64_t)-1), (int64_t)INT32_MAX - 1);
+        const int vhi = !rok ? INT32_MAX : p < 0 ? 0 : min(p + 1, q.len);
+        const int vlo = rok && P.window ? max(p - P.window + 1, 0) : 0;
+        const int vpre = rok && p >= 0 ? q.pre : 0;
+        const float slope = EXTRA && P.slopes ? __ldg(P.slopes + head) : 0.f;
+        const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
+        float qs;
+        {
+            const float* y = P.q + qrow * P.ld_q + (int64_t)head * D;
+            const bool vec = ((reinterpret_cast<uintptr_t>(P.q) | (uintptr_t)(P.ld_q * 4)) & 15) == 0;
+            auto ld4 = [&](int d) {
+                if (!rok) return make_float4(0.f, 0.f, 0.f, 0.f);
+                return vec ? __ldg(reinterpret_cast<const float4*>(y + d))
+                           : make_float4(__ldg(y + d), __ldg(y + d + 1), __ldg(y + d + 2), __ldg(y + d + 3));
+            };
+            float mx = 0.f;
+#pragma unroll 8
+            for (int d = 0; d < D; d += 4) {
+                const float4 v = ld4(d);
+                mx = fmaxf(mx, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+            }
+            const int es = max(1, (int)((__float_as_uint(mx) >> 23) & 0xFFu) - 14);     // |q| / 2^(es - 127) < 2^15
+            // the sign of the scale goes into q: the maximum of S is that of the scores then
+            const float inv = copysignf(__uint_as_float((uint32_t)(254 - es) << 23), P.scale);
+            qs = __uint_as_float((uint32_t)es << 23) * fabsf(P.scale) * (EXTRA ? 1.f : ATT_LOG2E);
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+                uint32_t h[16], l[16];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float4 v = ld4(d + 4 * e);
+                    att_split(v.x * inv, v.y * inv, h[2 * e], l[2 * e]);
+                    att_split(v.z * inv, v.w * inv, h[2 * e + 1], l[2 * e + 1]);
+                }
+                t_st16(trow + F::T_QH + d / 2, h);
+                if (!F::QLO_SMEM) {
+                    t_st16(trow + F::T_QL + d / 2, l);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sts128(sbase + F::Q_OFF + (r >> 3) * F::SBO_K + (d / 8 + e) * 128 + (r & 7) * 16, l[4 * e], l[4 * e + 1],
+                               l[4 * e + 2], l[4 * e + 3]);
+                }
+            }
+            t_wait_st();
+            if (F::QLO_SMEM) fence_proxy_async_smem();
+            t_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full);
+        }
+        float ref = -INFINITY, l = 0.f;
+        for (int j = 0; j < nt; ++j) {
+            const int b = j & 1, k0 = key0(j);
+            const uint32_t ph = (uint32_t)(j >> 1) & 1, ts = trow + F::T_S + b * NK, mt = meta + (j & 3) * NG * 16;
+            if (!(ok = pf_wait(&s_full[b], ph, P.timeout_ns))) break;
+            t_after();
+            const bool whole = k0 + NK <= vpre || (k0 >= vlo && k0 + NK <= vhi);
+            const bool plain = !EXTRA && __all_sync(0xFFFFFFFFu, whole);
+            // pass 1: the maximum (and, where the scores are more than one
+            // multiply-add of S, the finished exponents back in place of S)
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < NK; c += 32) {
+                uint32_t v[32];
+                const float4 m0 = lds4(mt + c), m1 = lds4(mt + c + 16);
+                t_ld32(ts + c, v);
+                if (plain) {
+                    float a = -INFINITY, bb = -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        a = fmaxf(a, __uint_as_float(v[e]));
+                        bb = fmaxf(bb, __uint_as_float(v[16 + e]));
+                    }
+                    mx = fmaxf(mx, fmaxf(fmaf(a, qs * m0.x, m0.y), fmaf(bb, qs * m1.x, m1.y)));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float4 mm = e < 16 ? m0 : m1;
+                        float u = __uint_as_float(v[e]) * (qs * mm.x);
+                        const int k = k0 + c + e;
+                        if (EXTRA) {
+                            if (P.softcap > 0.f) u = P.softcap * att_tanh(__fdividef(u, P.softcap));
+                            u -= slope * fabsf((float)(p - k));
+                            u *= ATT_LOG2E;
+                        }
+                        u += mm.y;
+                        if (!(k < vpre || (k >= vlo && k < vhi))) u = -INFINITY;
+                        v[e] = __float_as_uint(u);
+                        mx = fmaxf(mx, u);
+                    }
+                    t_st32(ts + c, v);
+                }
+            }
+            if (!plain) t_wait_st();
+            // the reference
+            const bool raise = mx > ref + PF_RAISE || (ref == -INFINITY && mx > -INFINITY);
+            if (__any_sync(0xFFFFFFFFu, raise)) {
+                const float f = raise ? (ref == -INFINITY ? 0.f : att_ex2(ref - mx)) : 1.f;
+                if (raise) ref = mx;
+                l *= f;
+                if (j > 0) {
+                    if (!(ok = pf_wait(&pv_done, (uint32_t)(j - 1) & 1, P.timeout_ns))) break;
+                    t_after();
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t v[32];
+                        t_ld32(trow + F::T_O + c, v);
+        #pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                        t_st32(trow + F::T_O + c, v);
+                    }
+                }
+            }
+            // pass 2: weights, their sums per 16 keys, their pieces
+            const float sub = ref == -INFINITY ? 0.f : ref - PF_SHIFT;
+#pragma unroll 1
+            for (int c = 0; c < NK; c += 32) {
+                uint32_t v[32], w[32];
+                const float4 m0 = lds4(mt + c), m1 = lds4(mt + c + 16);
+                t_ld32(ts + c, v);
+                const float f0 = plain ? qs * m0.x : 1.f, f1 = plain ? qs * m1.x : 1.f;
+                const float a0 = plain ? m0.y - sub : -sub, a1 = plain ? m1.y - sub : -sub;
+                float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float fe = e < 8 ? f0 : f1, ae = e < 8 ? a0 : a1;
+                    const float y0 = att_ex2(fmaf(__uint_as_float(v[2 * e]), fe, ae)), y1 = att_ex2(fmaf(__uint_as_float(v[2 * e + 1]), fe, ae));
+                    if (e < 8) s0 += y0 + y1;
+                    else s1 += y0 + y1;
+                    att_split(y0, y1, w[e], w[16 + e]);
+                }
+                // (a page that no visible key lies on may have a NaN scale)
+                if (!(s0 == 0.f)) l = fmaf(s0, m0.z, l);
+                if (!(s1 == 0.f)) l = fmaf(s1, m1.z, l);
+                t_st32(ts + c, w);                            // hi of 32 keys, then lo
+            }
+            t_wait_st();
+            t_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[b]);
+        }
+        // ---- output.  PV(nt - 2) may be running still (S(nt - 1) followed
+        // PV(nt - 3)); a parity tells the next phase only, so both are waited for
+        if (ok && nt > 1) ok = pf_wait(&pv_done, (uint32_t)(nt - 2) & 1, P.timeout_ns);
+        if (ok && (ok = pf_wait(&pv_done, (uint32_t)(nt - 1) & 1, P.timeout_ns))) {
+            t_after();
+            const float f = l == 0.f ? 0.f : att_pow2(e0) / l;
+            float* y = P.out + qrow * P.ld_out + (int64_t)head * D;
+            const bool vec = ((reinterpret_cast<uintptr_t>(P.out) | (uintptr_t)(P.ld_out * 4)) & 15) == 0;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t v[32];
+                t_ld32(trow + F::T_O + c, v);
+                if (rok) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 o = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                                  : make_float4(__uint_as_float(v[e]) * f, __uint_as_float(v[e + 1]) * f,
+                                                                __uint_as_float(v[e + 2]) * f, __uint_as_float(v[e + 3]) * f);
+                        if (vec) {
+                            *reinterpret_cast<float4*>(y + c + e) = o;
+                        } else {
+                            y[c + e] = o.x;
+                            y[c + e + 1] = o.y;
+                            y[c + e + 2] = o.z;
+                            y[c + e + 3] = o.w;
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    } else if (warp < PF_MMA_WARP) {
+        // ---- converters: warp = a group of 16 keys (or half of its dims)
+        const int cw = warp - 4, g = cw / F::WPG, half = cw % F::WPG;
+        constexpr int NKU = 2 * (D / 64) / F::WPG, NVU = D / 32 / F::WPG;    // 16-byte pieces per lane of K, of V
+        const int pmask = (1 << P.c.pshift) - 1;
+        const int64_t blk = (int64_t)D << P.c.pshift;
+        const float is = att_pow2(-e0);
+        uint4 kr[NKU], vr[NVU];
+        float ks = 0.f, vs = 0.f;
+        int pg, pnext;
+        auto page = [&](int j) {                              // of this group in tile j
+            const int pos = key0(j) + 16 * g;
+            return j < nt && pos < hi ? att_page(P, s, pos) : -1;
+        };
+        auto load = [&](int j, int pgj) {
+            const int off = (key0(j) + 16 * g) & pmask;
+            const int64_t ph = (int64_t)pgj * P.c.n_kv + hk;
+            const int8_t* kp = P.c.k + ph * blk + (int64_t)off * D;
+            const int8_t* vp = P.c.v + ph * blk + off;
+#pragma unroll
+            for (int i = 0; i < NKU; ++i) {
+                const int key = (i & 1) * 8 + (lane & 7), u = (half * (NKU / 2) + (i >> 1)) * 4 + (lane >> 3);
+                kr[i] = pgj >= 0 ? __ldg(reinterpret_cast<const uint4*>(kp + key * D + u * 16)) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < NVU; ++i) {
+                const int d = (half * NVU + i) * 32 + lane;
+                vr[i] = pgj >= 0 ? __ldg(reinterpret_cast<const uint4*>(vp + ((int64_t)d << P.c.pshift))) : make_uint4(0, 0, 0, 0);
+            }
+            ks = pgj >= 0 ? __ldg(P.c.ks + ph) : 0.f;
+            vs = pgj >= 0 ? __ldg(P.c.vs + ph) : 0.f;
+        };
+        pg = page(0);
+        load(0, pg);
+        pnext = page(1);
+        for (int j = 0; j < nt; ++j) {
+            const int b = j & 1, k0 = key0(j) + 16 * g;
+            const uint32_t ph = (uint32_t)(j >> 1) & 1;
+            if (pg < 0 && k0 < hi && lane == 0 && half == 0) {
+                // keys without a page: does a row see one of them?
+                const int a = max(k0, lo), e = min(k0 + 16, hi);
+                const bool seen = k0 < min(q.pre, hi) || (a < e && a <= p1);
+                if (seen) record_status(P.status, STATUS_BADARG);
+            }
+            bool vzero;
+            const float rel = att_rel(vs * is, vzero);
+            if (j >= 2 && !(ok = pf_wait(&k_free[b], ph ^ 1, P.timeout_ns))) break;
+            if (lane == 0 && half == 0)
+                sts128(meta + ((j & 3) * NG + g) * 16, __float_as_uint(ks), __float_as_uint(pg < 0 ? -INFINITY : att_lg2(rel)),
+                       __float_as_uint(att_rcp(rel)), 0u);
+            {
+                const uint32_t dst = sbase + F::K_OFF + b * F::KB + 2 * g * F::SBO_K;
+#pragma unroll
+                for (int i = 0; i < NKU; ++i) {
+                    const int u = (half * (NKU / 2) + (i >> 1)) * 4 + (lane >> 3);
+                    const uint32_t a = dst + (i & 1) * F::SBO_K + 2 * u * 128 + (lane & 7) * 16;
+                    uint32_t h[8];
+                    att_codes(kr[i].x, h[0], h[1]);
+                    att_codes(kr[i].y, h[2], h[3]);
+                    att_codes(kr[i].z, h[4], h[5]);
+                    att_codes(kr[i].w, h[6], h[7]);
+                    sts128(a, h[0], h[1], h[2], h[3]);
+                    sts128(a + 128, h[4], h[5], h[6], h[7]);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&k_full[b]);
+            if (j >= 2 && !(ok = pf_wait(&v_free[b], ph ^ 1, P.timeout_ns))) break;
+            {
+                const uint32_t dst = sbase + F::V_OFF + b * F::KB + 2 * g * 128;
+#pragma unroll
+                for (int i = 0; i < NVU; ++i) {
+                    const int d = (half * NVU + i) * 32 + lane;
+                    const uint32_t a = dst + (d >> 3) * F::SBO_V + (d & 7) * 16;
+                    if (vzero) vr[i] = make_uint4(0, 0, 0, 0);
+                    uint32_t h[8];
+                    att_codes(vr[i].x, h[0], h[1]);
+                    att_codes(vr[i].y, h[2], h[3]);
+                    att_codes(vr[i].z, h[4], h[5]);
+                    att_codes(vr[i].w, h[6], h[7]);
+                    sts128(a, h[0], h[1], h[2], h[3]);
+                    sts128(a + 128, h[4], h[5], h[6], h[7]);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&v_full[b]);
+            pg = pnext;
+            if (j + 1 < nt) {
+                load(j + 1, pg);
+                pnext = page(j + 2);
+            }
+        }
+    } else if (lane == 0) {
+        // ---- MMA issue
+        const uint64_t kd = pf_desc(sbase + F::K_OFF, F::SBO_K), vd = pf_desc(sbase + F::V_OFF, F::SBO_V);
+        const uint64_t qd = pf_desc(sbase + F::Q_OFF, F::SBO_K);
+        auto mma_s = [&](int j) -> bool {
+            const int b = j & 1;
+            if (!mbar_wait_bounded(&k_full[b], (uint32_t)(j >> 1) & 1, P.timeout_ns)) return false;
+            t_after();
+            const uint32_t d = tmem + F::T_S + b * NK;
+            const uint64_t kb = kd + (b * F::KB >> 4);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) pf_mma_ts(d, tmem + F::T_QH + 8 * i, kb + 16 * i, pf_idesc(NK), i > 0);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                if (F::QLO_SMEM) pf_mma_ss(d, qd + 16 * i, kb + 16 * i, pf_idesc(NK), 1);
+                else pf_mma_ts(d, tmem + F::T_QL + 8 * i, kb + 16 * i, pf_idesc(NK), 1);
+            }
+            pf_commit(&s_full[b]);
+            pf_commit(&k_free[b]);
+            return true;
+        };
+        ok = mbar_wait_bounded(&q_full, 0, P.timeout_ns);
+        t_after();
+        ok = ok && mma_s(0) && (nt < 2 || mma_s(1));
+        for (int j = 0; ok && j < nt; ++j) {
+            const int b = j & 1;
+            ok = mbar_wait_bounded(&p_full[b], (uint32_t)(j >> 1) & 1, P.timeout_ns) &&
+                 mbar_wait_bounded(&v_full[b], (uint32_t)(j >> 1) & 1, P.timeout_ns);
+            if (!ok) break;
+            t_after();
+            const uint32_t a = tmem + F::T_S + b * NK;
+            const uint64_t vb = vd + (b * F::KB >> 4);
+#pragma unroll
+            for (int i = 0; i < NK / 16; ++i) {
+                const uint32_t ai = a + 32 * (i >> 1) + 8 * (i & 1);
+                pf_mma_ts(tmem + F::T_O, ai, vb + 16 * i, pf_idesc(D), (j | i) != 0);
+                pf_mma_ts(tmem + F::T_O, ai + 16, vb + 16 * i, pf_idesc(D), 1);
+            }
+            pf_commit(&v_free[b]);
+            pf_commit(&pv_done);
+            // S(j + 2) is written over the weights that PV(j) reads
+            if (j + 2 < nt) ok = mbar_wait_bounded(&pv_done, (uint32_t)j & 1, P.timeout_ns) && mma_s(j + 2);
+        }
+    }
+    if (!ok && lane == 0) record_status(P.status, STATUS_TIMEOUT);
+    if (warp == PF_MMA_WARP) {
+        // every MMA issued has ended before the tensor memory goes
+        if (lane == 0) {
+            pf_commit(&q_full);                               // (its first phase has long been used; 4 arrivals make the next)
+            mbar_arrive(&q_full);
+            mbar_arrive(&q_full);
+            mbar_arrive(&q_full);
+            if (!mbar_wait_bounded(&q_full, 1, drain_bound(P.timeout_ns))) record_status(P.status, STATUS_TIMEOUT);
+        }
+        __syncwarp();
+    }
+    t_before();
+    __syncthreads();
+    t_after();
+    if (warp == PF_MMA_WARP) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+template <int D>
+cudaError_t prefill_launch(const AttnParams& P, cudaStream_t st) {
+    using F = Pf<D>;
+    const bool extra = P.softcap > 0.f || P.slopes;
+    auto kern = extra ? kv8_prefill_kernel<D, true> : kv8_prefill_kernel<D, false>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F::SMEM);
+    if (e != cudaSuccess) return e;
+    // at least as many tiles as any split of the rows over the sequences gives
+    const int64_t tiles = (((int64_t)P.s.ntok * (P.n_q / P.c.n_kv)) >> 7) + P.s.nseq;
+    if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+    kern<<<dim3((unsigned)tiles, (unsigned)P.c.n_kv), PF_THREADS, F::SMEM, st>>>(P);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_prefill(const AttnParams& P, cudaStream_t st) {
+    return P.c.d == 64 ? prefill_launch<64>(P, st) : P.c.d == 128 ? prefill_launch<128>(P, st) : prefill_launch<256>(P, st);
+}
+
+}  // namespace lq
