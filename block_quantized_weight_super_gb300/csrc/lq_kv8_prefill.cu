@@ -17,17 +17,27 @@
 // (D = 256 has no room there for the lo pieces of Q: those stay in shared
 // memory.)
 //
-// Softmax.  Thread r of warps 0-3 owns row r (tensor-memory lane r).  A first
-// pass over S finds the tile's maximum, a second one forms the weights and
-// writes their pieces.  The scales of a page enter as one factor and one
-// summand per 16 keys: weight = 2^(S qs ks + log2(vs / 2^e0) - ref), so V is
-// used as codes; the row sum divides the value scale out again per 16 keys.
-// ref is the row's maximum when it was last set; it is raised, and O rescaled,
-// only when a tile exceeds it by 2^4, so O is rarely touched.
+// Softmax.  A thread owns a row (a tensor-memory lane).  Warps 0-3 take the
+// even tiles, 4-7 the odd ones, so each has two tiles' time for one (with one
+// group of four the tensor cores waited for it: 390 us for the 4096-token
+// prompt against 250).  A first pass over S finds the tile's maximum, a second
+// one forms the weights and writes their pieces.  The scales of a page enter
+// as one factor and one summand per 16 keys: weight = 2^(S qs ks + log2(vs /
+// 2^e0) - ref), so V is used as codes; the row sum divides the value scale out
+// again per 16 keys.  ref is the row's maximum when it was last set; it is
+// raised, and O rescaled, only when a tile exceeds it by 2^4.  It goes from
+// tile to tile through shared memory, right after the first pass; the sums of
+// the two groups are joined at the end.
 //
-// Warps.  0-3 softmax (one per scheduler), 4-11 converters: each takes the
-// codes of 16 keys (one page) of a tile from global memory through registers,
-// a tile ahead, into fp16 in the MMA's core-matrix layout; 12 issues the MMAs.
+// Rounding.  The tensor cores truncate when they add to an accumulator, which
+// over thousands of keys shrinks O by 2e-8 per MMA (7e-6 after 3000 keys).  So O
+// starts anew every G tiles (32 MMAs), and the softmax threads add it up in
+// fp32: in shared memory, or for D = 256, where there is no room, in the output
+// rows.
+//
+// Warps.  0-7 softmax, 8-11 converters: each takes the codes of 16-key groups
+// (one page each) of a tile from global memory through registers, a tile
+// ahead, into fp16 in the MMA's core-matrix layout; 12 issues the MMAs.
 // Tensor order: PV(j), S(j + 2), PV(j + 1), ...: while PV(j) and S(j + 2) run the
 // softmax works on tile j + 1.
 //
@@ -39,9 +49,9 @@ namespace lq {
 namespace {
 
 constexpr int PF_ROWS = 128;
-constexpr int PF_CONV = 8;                                   // converter warps
-constexpr int PF_THREADS = (4 + PF_CONV + 1) * 32;
-constexpr int PF_MMA_WARP = 4 + PF_CONV;
+constexpr int PF_SOFT = 8, PF_CONV = 4;                      // softmax, converter warps
+constexpr int PF_MMA_WARP = PF_SOFT + PF_CONV;
+constexpr int PF_THREADS = (PF_MMA_WARP + 1) * 32;
 // Weights are 2^(u - ref + 11), at most 2^15: the lo pieces' floor of 2^-25 is
 // 2^-36 of the row's largest weight or less.
 constexpr float PF_SHIFT = 11.f;
@@ -51,11 +61,14 @@ template <int D>
 struct Pf {
     static constexpr int NK = D == 256 ? 64 : 128;           // keys of a tile
     static constexpr int NG = NK / 16;                       // 16-key groups
-    static constexpr int WPG = PF_CONV / NG;                 // converter warps of a group
+    static constexpr int GPW = NG / PF_CONV;                 // groups of a converter warp
+    static constexpr int G = D == 256 ? 4 : 2;               // tiles between two flushes of O (even: warps 0-3 do them)
     static constexpr bool QLO_SMEM = D == 256;
     static constexpr uint32_t KB = NK * D * 2;               // bytes of a K or V tile
     static constexpr uint32_t K_OFF = 0, V_OFF = 2 * KB, Q_OFF = 4 * KB;
-    static constexpr uint32_t META_OFF = Q_OFF + (QLO_SMEM ? PF_ROWS * D * 2 : 0);
+    static constexpr bool SUM_SMEM = D <= 128;               // where flushed O goes: [D][rows] fp32, or the output
+    static constexpr uint32_t SUM_OFF = Q_OFF + (QLO_SMEM ? PF_ROWS * D * 2 : 0);
+    static constexpr uint32_t META_OFF = SUM_OFF + (SUM_SMEM ? PF_ROWS * D * 4 : 0);
     // (ks, log2, 1 / rel) of the groups of 4 tiles; and one CTA per SM, as each takes all of the tensor memory
     static constexpr uint32_t SMEM = META_OFF + 4 * NG * 16 > 120 * 1024 ? META_OFF + 4 * NG * 16 : 120 * 1024;
     // tensor memory columns
@@ -126,6 +139,29 @@ __device__ __forceinline__ float4 lds4(uint32_t a) {
     return v;
 }
 
+__device__ __forceinline__ float pf_lds(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ void pf_sts(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
+__device__ __forceinline__ float4 pf_ld4(const float* y, bool vec) {
+    return vec ? *reinterpret_cast<const float4*>(y) : make_float4(y[0], y[1], y[2], y[3]);
+}
+__device__ __forceinline__ void pf_st4(float* y, float4 o, bool vec) {
+    if (vec) {
+        *reinterpret_cast<float4*>(y) = o;
+    } else {
+        y[0] = o.x;
+        y[1] = o.y;
+        y[2] = o.z;
+        y[3] = o.w;
+    }
+}
+__device__ __forceinline__ float4 pf_fma4(float4 a, float b, float4 c) {
+    return make_float4(fmaf(a.x, b, c.x), fmaf(a.y, b, c.y), fmaf(a.z, b, c.z), fmaf(a.w, b, c.w));
+}
+
 // Lane 0 waits (32 lanes polling one barrier serialise on it), the warp follows.
 __device__ __forceinline__ bool pf_wait(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
     bool ok = true;
@@ -139,7 +175,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
     using F = Pf<D>;
     constexpr int NK = F::NK, NG = F::NG;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], pv_done, q_full;
+    __shared__ uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], pv_done, q_full, o_done;
+    __shared__ uint64_t ref_full[4], fin[4];                 // per warp of rows: a tile's reference is out; the odd tiles are done
+    __shared__ float refs[PF_ROWS], lodd[PF_ROWS], lrodd[PF_ROWS];
     __shared__ uint32_t tslot;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int grp = P.n_q / P.c.n_kv, hk = blockIdx.y;
@@ -182,8 +220,13 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
         }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&ref_full[i], 1);
+            mbar_init(&fin[i], 1);
+        }
         mbar_init(&pv_done, 1);
-        mbar_init(&q_full, 4);
+        mbar_init(&o_done, 1);
+        mbar_init(&q_full, PF_SOFT);
         fence_mbar_init();
     }
     if (warp == PF_MMA_WARP) {
@@ -196,9 +239,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
     const uint32_t tmem = tslot, sbase = smem_u32(smem), meta = sbase + F::META_OFF;
     bool ok = true;
 
-    if (warp < 4) {
-        // ---- softmax: thread = row
-        const int r = warp * 32 + lane;
+    if (warp < PF_SOFT) {
+        // ---- softmax: thread = row, warps 0-3 even tiles, 4-7 odd ones
+        const int wg = warp >> 2, w4 = warp & 3, r = w4 * 32 + lane;
         const bool rok = r < rows;
         const int64_t rr = rt0 + (rok ? r : 0);
         const int head = hk * grp + (int)(rr % grp);
@@ -209,7 +252,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
         const int vlo = rok && P.window ? max(p - P.window + 1, 0) : 0;
         const int vpre = rok && p >= 0 ? q.pre : 0;
         const float slope = EXTRA && P.slopes ? __ldg(P.slopes + head) : 0.f;
-        const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
+        const uint32_t trow = tmem + ((uint32_t)(w4 * 32) << 16);
         float qs;
         {
             const float* y = P.q + qrow * P.ld_q + (int64_t)head * D;
@@ -230,7 +273,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
             const float inv = copysignf(__uint_as_float((uint32_t)(254 - es) << 23), P.scale);
             qs = __uint_as_float((uint32_t)es << 23) * fabsf(P.scale) * (EXTRA ? 1.f : ATT_LOG2E);
 #pragma unroll 1
-            for (int d = 0; d < D; d += 32) {
+            for (int d = wg * (D / 2); d < (wg + 1) * (D / 2); d += 32) {
                 uint32_t h[16], l[16];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -254,11 +297,15 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full);
         }
-        float ref = -INFINITY, l = 0.f;
-        for (int j = 0; j < nt; ++j) {
-            const int b = j & 1, k0 = key0(j);
-            const uint32_t ph = (uint32_t)(j >> 1) & 1, ts = trow + F::T_S + b * NK, mt = meta + (j & 3) * NG * 16;
-            if (!(ok = pf_wait(&s_full[b], ph, P.timeout_ns))) break;
+        float l = 0.f, lref = -INFINITY;                      // this group's sum, and the reference that it is in
+        float sref = -INFINITY;                               // the one that the flushed O is in
+        float* const yrow = P.out + qrow * P.ld_out + (int64_t)head * D;
+        const bool ovec = ((reinterpret_cast<uintptr_t>(P.out) | (uintptr_t)(P.ld_out * 4)) & 15) == 0;
+        const uint32_t sum = sbase + F::SUM_OFF + r * 4;
+        for (int j = wg; j < nt; j += 2) {
+            const int k0 = key0(j);
+            const uint32_t ts = trow + F::T_S + wg * NK, mt = meta + (j & 3) * NG * 16;
+            if (!(ok = pf_wait(&s_full[wg], (uint32_t)(j >> 1) & 1, P.timeout_ns))) break;
             t_after();
             const bool whole = k0 + NK <= vpre || (k0 >= vlo && k0 + NK <= vhi);
             const bool plain = !EXTRA && __all_sync(0xFFFFFFFFu, whole);
@@ -298,24 +345,20 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
                 }
             }
             if (!plain) t_wait_st();
-            // the reference
-            const bool raise = mx > ref + PF_RAISE || (ref == -INFINITY && mx > -INFINITY);
-            if (__any_sync(0xFFFFFFFFu, raise)) {
-                const float f = raise ? (ref == -INFINITY ? 0.f : att_ex2(ref - mx)) : 1.f;
-                if (raise) ref = mx;
-                l *= f;
-                if (j > 0) {
-                    if (!(ok = pf_wait(&pv_done, (uint32_t)(j - 1) & 1, P.timeout_ns))) break;
-                    t_after();
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t v[32];
-                        t_ld32(trow + F::T_O + c, v);
-        #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-                        t_st32(trow + F::T_O + c, v);
-                    }
-                }
+            // the reference: the last tile's, or raised
+            float before = -INFINITY;
+            if (j > 0) {
+                if (!(ok = pf_wait(&ref_full[w4], (uint32_t)(j - 1) & 1, P.timeout_ns))) break;
+                before = *(volatile float*)&refs[r];
+            }
+            const bool raise = mx > before + PF_RAISE || (before == -INFINITY && mx > -INFINITY);
+            const float ref = raise ? mx : before;
+            *(volatile float*)&refs[r] = ref;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ref_full[w4]);
+            if (lref != ref) {
+                l *= lref == -INFINITY ? 0.f : att_ex2(lref - ref);
+                lref = ref;
             }
             // pass 2: weights, their sums per 16 keys, their pieces
             const float sub = ref == -INFINITY ? 0.f : ref - PF_SHIFT;
@@ -323,151 +366,219 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
             for (int c = 0; c < NK; c += 32) {
                 uint32_t v[32], w[32];
                 const float4 m0 = lds4(mt + c), m1 = lds4(mt + c + 16);
-                t_ld32(ts + c, v);
                 const float f0 = plain ? qs * m0.x : 1.f, f1 = plain ? qs * m1.x : 1.f;
                 const float a0 = plain ? m0.y - sub : -sub, a1 = plain ? m1.y - sub : -sub;
-                float s0 = 0.f, s1 = 0.f;
+                t_ld32(ts + c, v);
+                float2 s0 = make_float2(0.f, 0.f), s1 = s0;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const float fe = e < 8 ? f0 : f1, ae = e < 8 ? a0 : a1;
-                    const float y0 = att_ex2(fmaf(__uint_as_float(v[2 * e]), fe, ae)), y1 = att_ex2(fmaf(__uint_as_float(v[2 * e + 1]), fe, ae));
-                    if (e < 8) s0 += y0 + y1;
-                    else s1 += y0 + y1;
-                    att_split(y0, y1, w[e], w[16 + e]);
+                    float2 y = __ffma2_rn(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), make_float2(fe, fe),
+                                          make_float2(ae, ae));
+                    y.x = att_ex2(y.x);
+                    y.y = att_ex2(y.y);
+                    if (e < 8) s0 = __fadd2_rn(s0, y);
+                    else s1 = __fadd2_rn(s1, y);
+                    const __half2 h = __floats2half2_rn(y.x, y.y);
+                    const float2 hf = __half22float2(h);
+                    const float2 lf = __fadd2_rn(y, make_float2(-hf.x, -hf.y));
+                    const __half2 lo2 = __floats2half2_rn(lf.x, lf.y);
+                    w[e] = *reinterpret_cast<const uint32_t*>(&h);
+                    w[16 + e] = *reinterpret_cast<const uint32_t*>(&lo2);
                 }
+                const float t0 = s0.x + s0.y, t1 = s1.x + s1.y;
                 // (a page that no visible key lies on may have a NaN scale)
-                if (!(s0 == 0.f)) l = fmaf(s0, m0.z, l);
-                if (!(s1 == 0.f)) l = fmaf(s1, m1.z, l);
+                if (!(t0 == 0.f)) l = fmaf(t0, m0.z, l);
+                if (!(t1 == 0.f)) l = fmaf(t1, m1.z, l);
                 t_st32(ts + c, w);                            // hi of 32 keys, then lo
+            }
+            // O, which PV(j) adds to: rescaled if a reference was raised,
+            // taken out if PV(j) begins it anew
+            const bool flush = j > 0 && j % F::G == 0;
+            if (j > 0 && (flush || __any_sync(0xFFFFFFFFu, raise))) {
+                if (!(ok = pf_wait(&pv_done, (uint32_t)(j - 1) & 1, P.timeout_ns))) break;
+                t_after();
+                const float f = raise ? (before == -INFINITY ? 0.f : att_ex2(before - ref)) : 1.f;
+                const bool more = j > F::G;                   // there is a sum from earlier flushes
+                const float gs = sref == -INFINITY ? 0.f : att_ex2(sref - ref);
+                if (flush) sref = ref;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t v[32];
+                    t_ld32(trow + F::T_O + c, v);
+                    if (!flush) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                        t_st32(trow + F::T_O + c, v);
+                    } else if (F::SUM_SMEM) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const uint32_t a = sum + (c + e) * (PF_ROWS * 4);
+                            const float o = __uint_as_float(v[e]) * f;
+                            pf_sts(a, more ? fmaf(pf_lds(a), gs, o) : o);
+                        }
+                    } else if (rok) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            float4 o = make_float4(__uint_as_float(v[e]) * f, __uint_as_float(v[e + 1]) * f,
+                                                   __uint_as_float(v[e + 2]) * f, __uint_as_float(v[e + 3]) * f);
+                            if (more) o = pf_fma4(pf_ld4(yrow + c + e, ovec), gs, o);
+                            pf_st4(yrow + c + e, o, ovec);
+                        }
+                    }
+                    __syncwarp();
+                }
             }
             t_wait_st();
             t_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[b]);
+            if (lane == 0) mbar_arrive(&p_full[wg]);
         }
-        // ---- output.  PV(nt - 2) may be running still (S(nt - 1) followed
-        // PV(nt - 3)); a parity tells the next phase only, so both are waited for
-        if (ok && nt > 1) ok = pf_wait(&pv_done, (uint32_t)(nt - 2) & 1, P.timeout_ns);
-        if (ok && (ok = pf_wait(&pv_done, (uint32_t)(nt - 1) & 1, P.timeout_ns))) {
-            t_after();
-            const float f = l == 0.f ? 0.f : att_pow2(e0) / l;
-            float* y = P.out + qrow * P.ld_out + (int64_t)head * D;
-            const bool vec = ((reinterpret_cast<uintptr_t>(P.out) | (uintptr_t)(P.ld_out * 4)) & 15) == 0;
+        if (wg == 1) {
+            *(volatile float*)&lodd[r] = l;
+            *(volatile float*)&lrodd[r] = lref;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&fin[w4]);
+        } else {
+            // ---- output.  (The last PV has a barrier of its own: which phase
+            // pv_done is in by now is not known, and a parity does not tell.)
+            ok = ok && pf_wait(&fin[w4], 0, P.timeout_ns) && pf_wait(&o_done, 0, P.timeout_ns);
+            if (ok) {
+                t_after();
+                const float ref = *(volatile float*)&refs[r], lr1 = *(volatile float*)&lrodd[r], l1 = *(volatile float*)&lodd[r];
+                if (lref != ref) l *= lref == -INFINITY ? 0.f : att_ex2(lref - ref);
+                l += lr1 == ref ? l1 : l1 * (lr1 == -INFINITY ? 0.f : att_ex2(lr1 - ref));
+                const float gs = sref == -INFINITY ? 0.f : att_ex2(sref - ref);
+                const bool more = nt > F::G;
+                const float f = l == 0.f ? 0.f : att_pow2(e0) / l;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t v[32];
-                t_ld32(trow + F::T_O + c, v);
-                if (rok) {
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t v[32];
+                    t_ld32(trow + F::T_O + c, v);
+                    if (rok) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 o = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                                  : make_float4(__uint_as_float(v[e]) * f, __uint_as_float(v[e + 1]) * f,
-                                                                __uint_as_float(v[e + 2]) * f, __uint_as_float(v[e + 3]) * f);
-                        if (vec) {
-                            *reinterpret_cast<float4*>(y + c + e) = o;
-                        } else {
-                            y[c + e] = o.x;
-                            y[c + e + 1] = o.y;
-                            y[c + e + 2] = o.z;
-                            y[c + e + 3] = o.w;
+                        for (int e = 0; e < 32; e += 4) {
+                            float4 o = make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), __uint_as_float(v[e + 2]),
+                                                   __uint_as_float(v[e + 3]));
+                            if (more) {
+                                float4 z;
+                                if (F::SUM_SMEM) {
+                                    const uint32_t a = sum + (c + e) * (PF_ROWS * 4);
+                                    z = make_float4(pf_lds(a), pf_lds(a + PF_ROWS * 4), pf_lds(a + 2 * PF_ROWS * 4), pf_lds(a + 3 * PF_ROWS * 4));
+                                } else {
+                                    z = pf_ld4(yrow + c + e, ovec);
+                                }
+                                o = pf_fma4(z, gs, o);
+                            }
+                            pf_st4(yrow + c + e, l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * f, o.y * f, o.z * f, o.w * f),
+                                   ovec);
                         }
                     }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
         }
     } else if (warp < PF_MMA_WARP) {
-        // ---- converters: warp = a group of 16 keys (or half of its dims)
-        const int cw = warp - 4, g = cw / F::WPG, half = cw % F::WPG;
-        constexpr int NKU = 2 * (D / 64) / F::WPG, NVU = D / 32 / F::WPG;    // 16-byte pieces per lane of K, of V
+        // ---- converters: warp = GPW groups of 16 keys
+        const int g0 = (warp - PF_SOFT) * F::GPW;
+        constexpr int GPW = F::GPW, NKU = D / 32, NVU = D / 32;    // 16-byte pieces per lane of a group's K, of its V
         const int pmask = (1 << P.c.pshift) - 1;
         const int64_t blk = (int64_t)D << P.c.pshift;
         const float is = att_pow2(-e0);
-        uint4 kr[NKU], vr[NVU];
-        float ks = 0.f, vs = 0.f;
-        int pg, pnext;
-        auto page = [&](int j) {                              // of this group in tile j
+        uint4 kr[GPW][NKU], vr[GPW][NVU];
+        float ks[GPW], vs[GPW];
+        int pg[GPW], pnext[GPW];
+        auto page = [&](int j, int g) {                       // of group g in tile j
             const int pos = key0(j) + 16 * g;
             return j < nt && pos < hi ? att_page(P, s, pos) : -1;
         };
-        auto load = [&](int j, int pgj) {
-            const int off = (key0(j) + 16 * g) & pmask;
-            const int64_t ph = (int64_t)pgj * P.c.n_kv + hk;
-            const int8_t* kp = P.c.k + ph * blk + (int64_t)off * D;
-            const int8_t* vp = P.c.v + ph * blk + off;
+        // K of tile j + 1 is on its way while V of tile j is converted, V of
+        // tile j + 1 while its K is
+        auto load_k = [&](int j) {
 #pragma unroll
-            for (int i = 0; i < NKU; ++i) {
-                const int key = (i & 1) * 8 + (lane & 7), u = (half * (NKU / 2) + (i >> 1)) * 4 + (lane >> 3);
-                kr[i] = pgj >= 0 ? __ldg(reinterpret_cast<const uint4*>(kp + key * D + u * 16)) : make_uint4(0, 0, 0, 0);
-            }
+            for (int x = 0; x < GPW; ++x) {
+                const bool has = pg[x] >= 0;
+                const int off = (key0(j) + 16 * (g0 + x)) & pmask;
+                const int64_t ph = (int64_t)pg[x] * P.c.n_kv + hk;
+                const int8_t* kp = P.c.k + ph * blk + (int64_t)(off + (lane & 7)) * D + (lane >> 3) * 16;
 #pragma unroll
-            for (int i = 0; i < NVU; ++i) {
-                const int d = (half * NVU + i) * 32 + lane;
-                vr[i] = pgj >= 0 ? __ldg(reinterpret_cast<const uint4*>(vp + ((int64_t)d << P.c.pshift))) : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < NKU; ++i)                 // keys (i & 1) 8 + lane % 8, dims 64 (i / 2) + 16 (lane / 8) ..
+                    kr[x][i] = has ? __ldg(reinterpret_cast<const uint4*>(kp + (i & 1) * 8 * D + (i >> 1) * 64)) : make_uint4(0, 0, 0, 0);
+                ks[x] = has ? __ldg(P.c.ks + ph) : 0.f;
+                vs[x] = has ? __ldg(P.c.vs + ph) : 0.f;
             }
-            ks = pgj >= 0 ? __ldg(P.c.ks + ph) : 0.f;
-            vs = pgj >= 0 ? __ldg(P.c.vs + ph) : 0.f;
         };
-        pg = page(0);
-        load(0, pg);
-        pnext = page(1);
-        for (int j = 0; j < nt; ++j) {
-            const int b = j & 1, k0 = key0(j) + 16 * g;
-            const uint32_t ph = (uint32_t)(j >> 1) & 1;
-            if (pg < 0 && k0 < hi && lane == 0 && half == 0) {
-                // keys without a page: does a row see one of them?
-                const int a = max(k0, lo), e = min(k0 + 16, hi);
-                const bool seen = k0 < min(q.pre, hi) || (a < e && a <= p1);
-                if (seen) record_status(P.status, STATUS_BADARG);
-            }
-            bool vzero;
-            const float rel = att_rel(vs * is, vzero);
-            if (j >= 2 && !(ok = pf_wait(&k_free[b], ph ^ 1, P.timeout_ns))) break;
-            if (lane == 0 && half == 0)
-                sts128(meta + ((j & 3) * NG + g) * 16, __float_as_uint(ks), __float_as_uint(pg < 0 ? -INFINITY : att_lg2(rel)),
-                       __float_as_uint(att_rcp(rel)), 0u);
-            {
-                const uint32_t dst = sbase + F::K_OFF + b * F::KB + 2 * g * F::SBO_K;
+        auto load_v = [&](int j) {
 #pragma unroll
-                for (int i = 0; i < NKU; ++i) {
-                    const int u = (half * (NKU / 2) + (i >> 1)) * 4 + (lane >> 3);
-                    const uint32_t a = dst + (i & 1) * F::SBO_K + 2 * u * 128 + (lane & 7) * 16;
-                    uint32_t h[8];
-                    att_codes(kr[i].x, h[0], h[1]);
-                    att_codes(kr[i].y, h[2], h[3]);
-                    att_codes(kr[i].z, h[4], h[5]);
-                    att_codes(kr[i].w, h[6], h[7]);
-                    sts128(a, h[0], h[1], h[2], h[3]);
-                    sts128(a + 128, h[4], h[5], h[6], h[7]);
+            for (int x = 0; x < GPW; ++x) {
+                const bool has = pg[x] >= 0;
+                const int off = (key0(j) + 16 * (g0 + x)) & pmask;
+                const int64_t ph = (int64_t)pg[x] * P.c.n_kv + hk;
+                const int8_t* vp = P.c.v + ph * blk + ((int64_t)lane << P.c.pshift) + off;
+#pragma unroll
+                for (int i = 0; i < NVU; ++i)                 // dim 32 i + lane
+                    vr[x][i] = has ? __ldg(reinterpret_cast<const uint4*>(vp + ((int64_t)(32 * i) << P.c.pshift))) : make_uint4(0, 0, 0, 0);
+            }
+        };
+        // a piece of 16 codes into two core-matrix rows
+        auto put = [&](uint32_t a, const uint4& c) {
+            uint32_t h[8];
+            att_codes(c.x, h[0], h[1]);
+            att_codes(c.y, h[2], h[3]);
+            att_codes(c.z, h[4], h[5]);
+            att_codes(c.w, h[6], h[7]);
+            sts128(a, h[0], h[1], h[2], h[3]);
+            sts128(a + 128, h[4], h[5], h[6], h[7]);
+        };
+#pragma unroll
+        for (int x = 0; x < GPW; ++x) pg[x] = page(0, g0 + x);
+        load_k(0);
+        load_v(0);
+#pragma unroll
+        for (int x = 0; x < GPW; ++x) pnext[x] = page(1, g0 + x);
+        for (int j = 0; j < nt; ++j) {
+            const int b = j & 1;
+            const uint32_t ph = (uint32_t)(j >> 1) & 1;
+            if (j >= 2 && !(ok = pf_wait(&k_free[b], ph ^ 1, P.timeout_ns))) break;
+            bool vzero[GPW];
+#pragma unroll
+            for (int x = 0; x < GPW; ++x) {
+                const int g = g0 + x, k0 = key0(j) + 16 * g;
+                const float rel = att_rel(vs[x] * is, vzero[x]);
+                if (lane == 0) {
+                    sts128(meta + ((j & 3) * NG + g) * 16, __float_as_uint(ks[x]), __float_as_uint(pg[x] < 0 ? -INFINITY : att_lg2(rel)),
+                           __float_as_uint(att_rcp(rel)), 0u);
+                    if (pg[x] < 0 && k0 < hi) {               // keys without a page: does a row see one of them?
+                        const int a = max(k0, lo), e = min(k0 + 16, hi);
+                        if (k0 < min(q.pre, hi) || (a < e && a <= p1)) record_status(P.status, STATUS_BADARG);
+                    }
                 }
+                const uint32_t dst = sbase + F::K_OFF + b * F::KB + 2 * g * F::SBO_K + 2 * (lane >> 3) * 128 + (lane & 7) * 16;
+#pragma unroll
+                for (int i = 0; i < NKU; ++i) put(dst + (i & 1) * F::SBO_K + (i >> 1) * 1024, kr[x][i]);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&k_full[b]);
-            if (j >= 2 && !(ok = pf_wait(&v_free[b], ph ^ 1, P.timeout_ns))) break;
-            {
-                const uint32_t dst = sbase + F::V_OFF + b * F::KB + 2 * g * 128;
+            if (j + 1 < nt) {
 #pragma unroll
-                for (int i = 0; i < NVU; ++i) {
-                    const int d = (half * NVU + i) * 32 + lane;
-                    const uint32_t a = dst + (d >> 3) * F::SBO_V + (d & 7) * 16;
-                    if (vzero) vr[i] = make_uint4(0, 0, 0, 0);
-                    uint32_t h[8];
-                    att_codes(vr[i].x, h[0], h[1]);
-                    att_codes(vr[i].y, h[2], h[3]);
-                    att_codes(vr[i].z, h[4], h[5]);
-                    att_codes(vr[i].w, h[6], h[7]);
-                    sts128(a, h[0], h[1], h[2], h[3]);
-                    sts128(a + 128, h[4], h[5], h[6], h[7]);
-                }
+                for (int x = 0; x < GPW; ++x) pg[x] = pnext[x];
+                load_k(j + 1);
+            }
+            if (j >= 2 && !(ok = pf_wait(&v_free[b], ph ^ 1, P.timeout_ns))) break;
+#pragma unroll
+            for (int x = 0; x < GPW; ++x) {
+                const uint32_t dst = sbase + F::V_OFF + b * F::KB + 2 * (g0 + x) * 128 + (lane >> 3) * F::SBO_V + (lane & 7) * 16;
+#pragma unroll
+                for (int i = 0; i < NVU; ++i) put(dst + 4 * i * F::SBO_V, vzero[x] ? make_uint4(0, 0, 0, 0) : vr[x][i]);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&v_full[b]);
-            pg = pnext;
             if (j + 1 < nt) {
-                load(j + 1, pg);
-                pnext = page(j + 2);
+                load_v(j + 1);
+#pragma unroll
+                for (int x = 0; x < GPW; ++x) pnext[x] = page(j + 2, g0 + x);
             }
         }
     } else if (lane == 0) {
@@ -480,13 +591,14 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
             t_after();
             const uint32_t d = tmem + F::T_S + b * NK;
             const uint64_t kb = kd + (b * F::KB >> 4);
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) pf_mma_ts(d, tmem + F::T_QH + 8 * i, kb + 16 * i, pf_idesc(NK), i > 0);
+            // (the lo pieces first: adding them to a large sum would truncate it once more each)
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
-                if (F::QLO_SMEM) pf_mma_ss(d, qd + 16 * i, kb + 16 * i, pf_idesc(NK), 1);
-                else pf_mma_ts(d, tmem + F::T_QL + 8 * i, kb + 16 * i, pf_idesc(NK), 1);
+                if (F::QLO_SMEM) pf_mma_ss(d, qd + 16 * i, kb + 16 * i, pf_idesc(NK), i > 0);
+                else pf_mma_ts(d, tmem + F::T_QL + 8 * i, kb + 16 * i, pf_idesc(NK), i > 0);
             }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) pf_mma_ts(d, tmem + F::T_QH + 8 * i, kb + 16 * i, pf_idesc(NK), 1);
             pf_commit(&s_full[b]);
             pf_commit(&k_free[b]);
             return true;
@@ -503,13 +615,14 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
             const uint32_t a = tmem + F::T_S + b * NK;
             const uint64_t vb = vd + (b * F::KB >> 4);
 #pragma unroll
-            for (int i = 0; i < NK / 16; ++i) {
-                const uint32_t ai = a + 32 * (i >> 1) + 8 * (i & 1);
-                pf_mma_ts(tmem + F::T_O, ai, vb + 16 * i, pf_idesc(D), (j | i) != 0);
-                pf_mma_ts(tmem + F::T_O, ai + 16, vb + 16 * i, pf_idesc(D), 1);
-            }
+            for (int h = 1; h >= 0; --h)                      // lo pieces, hi pieces
+#pragma unroll
+                for (int i = 0; i < NK / 16; ++i)
+                    pf_mma_ts(tmem + F::T_O, a + 32 * (i >> 1) + 8 * (i & 1) + 16 * h, vb + 16 * i, pf_idesc(D),
+                              h == 0 || i > 0 || j % F::G != 0);
             pf_commit(&v_free[b]);
             pf_commit(&pv_done);
+            if (j == nt - 1) pf_commit(&o_done);
             // S(j + 2) is written over the weights that PV(j) reads
             if (j + 2 < nt) ok = mbar_wait_bounded(&pv_done, (uint32_t)j & 1, P.timeout_ns) && mma_s(j + 2);
         }
@@ -518,10 +631,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
     if (warp == PF_MMA_WARP) {
         // every MMA issued has ended before the tensor memory goes
         if (lane == 0) {
-            pf_commit(&q_full);                               // (its first phase has long been used; 4 arrivals make the next)
-            mbar_arrive(&q_full);
-            mbar_arrive(&q_full);
-            mbar_arrive(&q_full);
+            // (q_full's first phase has long been used: the rest of a second one)
+            for (int i = 1; i < PF_SOFT; ++i) mbar_arrive(&q_full);
+            pf_commit(&q_full);
             if (!mbar_wait_bounded(&q_full, 1, drain_bound(P.timeout_ns))) record_status(P.status, STATUS_TIMEOUT);
         }
         __syncwarp();
