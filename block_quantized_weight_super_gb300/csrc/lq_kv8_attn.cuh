@@ -32,6 +32,16 @@ __device__ __forceinline__ float att_rcp(float x) {
     return y;
 }
 
+// mbar_wait_bounded, but the clock that bounds it is read only after a number
+// of tries (each suspends for a while in hardware): reading it costs about a
+// microsecond, which would be the least that any wait takes.
+__device__ __forceinline__ bool att_wait(uint64_t* bar, unsigned parity, uint64_t timeout_ns) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait_bounded(bar, parity, timeout_ns);
+}
+
 // tanh to fp32 rounding: an odd polynomial (least-squares fit of tanh(x) / x
 // in x^2, relative error 3e-9) up to 0.6, where 1 - 2 / (e^2x + 1) would
 // cancel, and that form beyond (its error is then below 2^-23 of the value).

@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(Dc<D, NR>::NT, 1) kv8_decode_kernel(const __gr
     auto arrived = [&](int h) -> bool {
         cs = cs + 1 == NSLOT ? 0 : cs + 1;
         cph ^= cs == 0;
-        if (__all_sync(0xFFFFFFFFu, mbar_wait_bounded(bars + cs, cph, P.timeout_ns))) return true;
+        if (__all_sync(0xFFFFFFFFu, att_wait(bars + cs, cph, P.timeout_ns))) return true;
         record_status(P.status, STATUS_TIMEOUT);
         for (int k = h; k < min(h + NSLOT - 1, 2 * nu); ++k)
             mbar_wait_bounded(bars + k % NSLOT, (uint32_t)((k / NSLOT) & 1), drain_bound(P.timeout_ns));

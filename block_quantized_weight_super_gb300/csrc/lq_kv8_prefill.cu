@@ -74,6 +74,11 @@ struct Pf {
     // tensor memory columns
     static constexpr uint32_t T_S = 0, T_O = 2 * NK, T_QH = T_O + D, T_QL = T_QH + D / 2;
     static_assert(T_QH + (QLO_SMEM ? D / 2 : D) <= 512, "tensor memory");
+    // q's pieces on their way: hi of row w in the second K buffer, lo in the second V buffer; D = 256: hi in both
+    __device__ static constexpr uint32_t stage_hi(int w) {
+        return D == 256 && w >= 64 ? V_OFF + KB + (w - 64) * D * 2 : K_OFF + KB + w * D * 2;
+    }
+    __device__ static constexpr uint32_t stage_lo(int w) { return V_OFF + KB + w * D * 2; }
     static constexpr uint32_t SBO_K = 16 * D, SBO_V = 16 * NK;    // core matrices of 8 rows; 128 bytes along K
 };
 
@@ -102,17 +107,35 @@ __device__ __forceinline__ void t_before() { asm volatile("tcgen05.fence::before
 __device__ __forceinline__ void t_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 #define LQ_R8(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), "=r"(x[i + 4]), "=r"(x[i + 5]), "=r"(x[i + 6]), "=r"(x[i + 7])
+#define LQ_W8(x, i) "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3]), "+r"(x[i + 4]), "+r"(x[i + 5]), "+r"(x[i + 6]), "+r"(x[i + 7])
 #define LQ_S8(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]), "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
-// The load and its wait in one statement: uses of v could otherwise be moved
-// between them.
+// A load of 32 columns, and the wait for all loads of the warp, which hands
+// the registers on (their uses cannot be moved before it).
 __device__ __forceinline__ void t_ld32(uint32_t a, uint32_t (&v)[32]) {
     asm volatile(
-        "{\n\ttcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;\n\t}"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
         : LQ_R8(v, 0), LQ_R8(v, 8), LQ_R8(v, 16), LQ_R8(v, 24)
         : "r"(a)
         : "memory");
+}
+__device__ __forceinline__ void t_wait32(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : LQ_W8(v, 0), LQ_W8(v, 8), LQ_W8(v, 16), LQ_W8(v, 24)::"memory");
+}
+// f(c, v) for the 32-column pieces c, c + 32 .. of N columns from `a` on.
+// Rolled: the loops of the roles share the instruction cache (unrolled
+// fully, with a piece on its way while another is worked on, a 4096-token prompt
+// took 487 us instead of 397).
+template <int N, class F>
+__device__ __forceinline__ void t_each32(uint32_t a, F f) {
+#pragma unroll 1
+    for (int c = 0; c < N; c += 32) {
+        uint32_t x[32];
+        t_ld32(a + c, x);
+        t_wait32(x);
+        f(c, x);
+    }
 }
 __device__ __forceinline__ void t_st32(uint32_t a, const uint32_t (&v)[32]) {
     asm volatile(
@@ -129,9 +152,16 @@ __device__ __forceinline__ void t_st16(uint32_t a, const uint32_t (&v)[16]) {
         : "memory");
 }
 #undef LQ_R8
+#undef LQ_W8
 #undef LQ_S8
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
+    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void lds128(uint32_t a, uint32_t& x, uint32_t& y, uint32_t& z, uint32_t& w) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x), "=r"(y), "=r"(z), "=r"(w) : "r"(a) : "memory");
 }
 __device__ __forceinline__ float4 lds4(uint32_t a) {
     float4 v;
@@ -165,7 +195,7 @@ __device__ __forceinline__ float4 pf_fma4(float4 a, float b, float4 c) {
 // Lane 0 waits (32 lanes polling one barrier serialise on it), the warp follows.
 __device__ __forceinline__ bool pf_wait(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
     bool ok = true;
-    if ((threadIdx.x & 31) == 0) ok = mbar_wait_bounded(bar, parity, timeout_ns);
+    if ((threadIdx.x & 31) == 0) ok = att_wait(bar, parity, timeout_ns);
     __syncwarp();
     return __shfl_sync(0xFFFFFFFFu, ok, 0);
 }
@@ -177,7 +207,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], pv_done, q_full, o_done;
     __shared__ uint64_t ref_full[4], fin[4];                 // per warp of rows: a tile's reference is out; the odd tiles are done
-    __shared__ float refs[PF_ROWS], lodd[PF_ROWS], lrodd[PF_ROWS];
+    __shared__ float refs[PF_ROWS], lodd[PF_ROWS], lrodd[PF_ROWS], qscale[PF_ROWS];
     __shared__ uint32_t tslot;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int grp = P.n_q / P.c.n_kv, hk = blockIdx.y;
@@ -192,7 +222,15 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
     const int64_t nrows = (int64_t)q.n * grp;
     if (rt0 >= nrows) return;
     const int rows = (int)min((int64_t)PF_ROWS, nrows - rt0);
-    const int i0 = (int)(rt0 / grp), i1 = (int)((rt0 + rows - 1) / grp);
+    // row w of the tile: token i0 + (h0 + w) / grp, head (h0 + w) % grp of the
+    // group (32-bit divisions: 64-bit ones took 10 us of every tile)
+    const int i0 = (int)(rt0 / grp), h0 = (int)(rt0 - (int64_t)i0 * grp);
+    const int i1 = i0 + (h0 + rows - 1) / grp;
+    auto row_of = [&](int w, int& head) -> int64_t {          // its row of q and out
+        const uint32_t y = (uint32_t)(h0 + w), i = y / (uint32_t)grp;
+        head = hk * grp + (int)(y - i * grp);
+        return q.row0 + i0 + (int)i;
+    };
     const int64_t p0 = max(q.start + i0, (int64_t)0), p1 = q.start + i1;    // positions of the rows that see anything
     // key tiles: [0, na) and from cb on, nt in all
     const int hi = p1 < 0 ? 0 : (int)min((int64_t)q.len, max(p1 + 1, (int64_t)q.pre));
@@ -202,8 +240,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
     auto key0 = [&](int j) { return (j < na ? j : cb + (j - na)) * NK; };
     if (nt == 0) {
         for (int64_t i = tid; i < (int64_t)rows * D; i += PF_THREADS) {
-            const int64_t r = rt0 + i / D;
-            P.out[(q.row0 + r / grp) * P.ld_out + (hk * grp + r % grp) * D + i % D] = 0.f;
+            int head;
+            const int64_t row = row_of((int)(i / D), head);
+            P.out[row * P.ld_out + (int64_t)head * D + i % D] = 0.f;
         }
         return;
     }
@@ -243,60 +282,86 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
         // ---- softmax: thread = row, warps 0-3 even tiles, 4-7 odd ones
         const int wg = warp >> 2, w4 = warp & 3, r = w4 * 32 + lane;
         const bool rok = r < rows;
-        const int64_t rr = rt0 + (rok ? r : 0);
-        const int head = hk * grp + (int)(rr % grp);
-        const int64_t qrow = q.row0 + rr / grp;
-        const int64_t pl = q.start + rr / grp;
+        int head;
+        const int64_t qrow = row_of(rok ? r : 0, head);
+        const int64_t pl = q.start + (qrow - q.row0);
         const int p = (int)min(max(pl, (int64_t)-1), (int64_t)INT32_MAX - 1);
         const int vhi = !rok ? INT32_MAX : p < 0 ? 0 : min(p + 1, q.len);
         const int vlo = rok && P.window ? max(p - P.window + 1, 0) : 0;
         const int vpre = rok && p >= 0 ? q.pre : 0;
         const float slope = EXTRA && P.slopes ? __ldg(P.slopes + head) : 0.f;
         const uint32_t trow = tmem + ((uint32_t)(w4 * 32) << 16);
-        float qs;
+        // q: whole rows by a warp (lanes along the dims), their pieces through
+        // shared memory (the second K and V buffers, free until q_full) to
+        // the rows' threads, and on to tensor memory.  16-byte pieces of a row
+        // are swizzled by the row.
         {
-            const float* y = P.q + qrow * P.ld_q + (int64_t)head * D;
             const bool vec = ((reinterpret_cast<uintptr_t>(P.q) | (uintptr_t)(P.ld_q * 4)) & 15) == 0;
-            auto ld4 = [&](int d) {
-                if (!rok) return make_float4(0.f, 0.f, 0.f, 0.f);
-                return vec ? __ldg(reinterpret_cast<const float4*>(y + d))
-                           : make_float4(__ldg(y + d), __ldg(y + d + 1), __ldg(y + d + 2), __ldg(y + d + 3));
-            };
-            float mx = 0.f;
-#pragma unroll 8
-            for (int d = 0; d < D; d += 4) {
-                const float4 v = ld4(d);
-                mx = fmaxf(mx, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
-            }
-            const int es = max(1, (int)((__float_as_uint(mx) >> 23) & 0xFFu) - 14);     // |q| / 2^(es - 127) < 2^15
-            // the sign of the scale goes into q: the maximum of S is that of the scores then
-            const float inv = copysignf(__uint_as_float((uint32_t)(254 - es) << 23), P.scale);
-            qs = __uint_as_float((uint32_t)es << 23) * fabsf(P.scale) * (EXTRA ? 1.f : ATT_LOG2E);
+            constexpr int RW = D == 64 ? 2 : 1, NP = D == 256 ? 2 : 1;       // rows of a load, loads of a row
+            constexpr int NR = PF_ROWS / PF_SOFT, NY = 8;                    // rows of a warp; loads of rows in flight
 #pragma unroll 1
-            for (int d = wg * (D / 2); d < (wg + 1) * (D / 2); d += 32) {
-                uint32_t h[16], l[16];
+            for (int y0 = 0; y0 < NR; y0 += NY * RW) {
+                float4 v[NY][NP];
+                int rw[NY];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float4 v = ld4(d + 4 * e);
-                    att_split(v.x * inv, v.y * inv, h[2 * e], l[2 * e]);
-                    att_split(v.z * inv, v.w * inv, h[2 * e + 1], l[2 * e + 1]);
+                for (int y = 0; y < NY; ++y) {
+                    rw[y] = warp * NR + y0 + y * RW + (D == 64 ? lane >> 4 : 0);
+                    int hw;
+                    const int64_t row = row_of(rw[y], hw);
+                    const float* x = P.q + row * P.ld_q + (int64_t)hw * D;
+#pragma unroll
+                    for (int h = 0; h < NP; ++h) {
+                        const float* w = x + 128 * h + 4 * (D == 64 ? lane & 15 : lane);
+                        v[y][h] = rw[y] >= rows ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                  : vec         ? __ldg(reinterpret_cast<const float4*>(w))
+                                                : make_float4(__ldg(w), __ldg(w + 1), __ldg(w + 2), __ldg(w + 3));
+                    }
                 }
-                t_st16(trow + F::T_QH + d / 2, h);
-                if (!F::QLO_SMEM) {
-                    t_st16(trow + F::T_QL + d / 2, l);
-                } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        sts128(sbase + F::Q_OFF + (r >> 3) * F::SBO_K + (d / 8 + e) * 128 + (r & 7) * 16, l[4 * e], l[4 * e + 1],
-                               l[4 * e + 2], l[4 * e + 3]);
+                for (int y = 0; y < NY; ++y) {
+                    float mx = 0.f;
+#pragma unroll
+                    for (int h = 0; h < NP; ++h)
+                        mx = fmaxf(mx, fmaxf(fmaxf(fabsf(v[y][h].x), fabsf(v[y][h].y)), fmaxf(fabsf(v[y][h].z), fabsf(v[y][h].w))));
+#pragma unroll
+                    for (int o = D == 64 ? 8 : 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+                    const int es = max(1, (int)((__float_as_uint(mx) >> 23) & 0xFFu) - 14);     // |q| / 2^(es - 127) < 2^15
+                    // the sign of the scale goes into q: the maximum of S is that of the scores then
+                    const float inv = copysignf(__uint_as_float((uint32_t)(254 - es) << 23), P.scale);
+                    if ((D == 64 ? lane & 15 : lane) == 0)
+                        qscale[rw[y]] = __uint_as_float((uint32_t)es << 23) * fabsf(P.scale) * (EXTRA ? 1.f : ATT_LOG2E);
+#pragma unroll
+                    for (int h = 0; h < NP; ++h) {
+                        uint32_t a, b, c, d;
+                        att_split(v[y][h].x * inv, v[y][h].y * inv, a, c);
+                        att_split(v[y][h].z * inv, v[y][h].w * inv, b, d);
+                        const int w = rw[y], pc = (16 * h) + ((D == 64 ? lane & 15 : lane) >> 1), half8 = (lane & 1) * 8;
+                        sts64(sbase + F::stage_hi(w) + ((pc ^ (w & 7)) << 4) + half8, a, b);
+                        if (!F::QLO_SMEM) sts64(sbase + F::stage_lo(w) + ((pc ^ (w & 7)) << 4) + half8, c, d);
+                        else sts64(sbase + F::Q_OFF + (w >> 3) * F::SBO_K + pc * 128 + (w & 7) * 16 + half8, c, d);
+                    }
                 }
             }
-            t_wait_st();
-            if (F::QLO_SMEM) fence_proxy_async_smem();
-            t_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&q_full);
         }
+        asm volatile("bar.sync 1, %0;" ::"n"(PF_SOFT * 32) : "memory");
+        const float qs = qscale[r];
+#pragma unroll 1
+        for (int d = wg * (D / 2); d < (wg + 1) * (D / 2); d += 32) {
+            uint32_t h[16], l[16];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int pc = ((d / 8 + e) ^ (r & 7)) << 4;
+                lds128(sbase + F::stage_hi(r) + pc, h[4 * e], h[4 * e + 1], h[4 * e + 2], h[4 * e + 3]);
+                if (!F::QLO_SMEM) lds128(sbase + F::stage_lo(r) + pc, l[4 * e], l[4 * e + 1], l[4 * e + 2], l[4 * e + 3]);
+            }
+            t_st16(trow + F::T_QH + d / 2, h);
+            if (!F::QLO_SMEM) t_st16(trow + F::T_QL + d / 2, l);
+        }
+        t_wait_st();
+        if (F::QLO_SMEM) fence_proxy_async_smem();
+        t_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full);
         float l = 0.f, lref = -INFINITY;                      // this group's sum, and the reference that it is in
         float sref = -INFINITY;                               // the one that the flushed O is in
         float* const yrow = P.out + qrow * P.ld_out + (int64_t)head * D;
@@ -312,20 +377,25 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
             // pass 1: the maximum (and, where the scores are more than one
             // multiply-add of S, the finished exponents back in place of S)
             float mx = -INFINITY;
-#pragma unroll 1
-            for (int c = 0; c < NK; c += 32) {
-                uint32_t v[32];
-                const float4 m0 = lds4(mt + c), m1 = lds4(mt + c + 16);
-                t_ld32(ts + c, v);
-                if (plain) {
-                    float a = -INFINITY, bb = -INFINITY;
+            if (plain) {
+                t_each32<NK>(ts, [&](int c, uint32_t (&v)[32]) {
+                    const float4 m0 = lds4(mt + c), m1 = lds4(mt + c + 16);
+                    float a[4];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        a = fmaxf(a, __uint_as_float(v[e]));
-                        bb = fmaxf(bb, __uint_as_float(v[16 + e]));
-                    }
-                    mx = fmaxf(mx, fmaxf(fmaf(a, qs * m0.x, m0.y), fmaf(bb, qs * m1.x, m1.y)));
-                } else {
+                    for (int e = 0; e < 4; ++e) a[e] = fmaxf(__uint_as_float(v[8 * e]), __uint_as_float(v[8 * e + 1]));
+#pragma unroll
+                    for (int i = 2; i < 8; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) a[e] = fmaxf(a[e], __uint_as_float(v[8 * e + i]));
+                    mx = fmaxf(mx, fmaxf(fmaf(fmaxf(a[0], a[1]), qs * m0.x, m0.y), fmaf(fmaxf(a[2], a[3]), qs * m1.x, m1.y)));
+                });
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < NK; c += 32) {
+                    uint32_t v[32];
+                    t_ld32(ts + c, v);
+                    const float4 m0 = lds4(mt + c), m1 = lds4(mt + c + 16);
+                    t_wait32(v);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         const float4 mm = e < 16 ? m0 : m1;
@@ -362,36 +432,32 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
             }
             // pass 2: weights, their sums per 16 keys, their pieces
             const float sub = ref == -INFINITY ? 0.f : ref - PF_SHIFT;
-#pragma unroll 1
-            for (int c = 0; c < NK; c += 32) {
-                uint32_t v[32], w[32];
-                const float4 m0 = lds4(mt + c), m1 = lds4(mt + c + 16);
-                const float f0 = plain ? qs * m0.x : 1.f, f1 = plain ? qs * m1.x : 1.f;
-                const float a0 = plain ? m0.y - sub : -sub, a1 = plain ? m1.y - sub : -sub;
-                t_ld32(ts + c, v);
-                float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+            t_each32<NK>(ts, [&](int c, uint32_t (&v)[32]) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float fe = e < 8 ? f0 : f1, ae = e < 8 ? a0 : a1;
-                    float2 y = __ffma2_rn(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), make_float2(fe, fe),
-                                          make_float2(ae, ae));
-                    y.x = att_ex2(y.x);
-                    y.y = att_ex2(y.y);
-                    if (e < 8) s0 = __fadd2_rn(s0, y);
-                    else s1 = __fadd2_rn(s1, y);
-                    const __half2 h = __floats2half2_rn(y.x, y.y);
-                    const float2 hf = __half22float2(h);
-                    const float2 lf = __fadd2_rn(y, make_float2(-hf.x, -hf.y));
-                    const __half2 lo2 = __floats2half2_rn(lf.x, lf.y);
-                    w[e] = *reinterpret_cast<const uint32_t*>(&h);
-                    w[16 + e] = *reinterpret_cast<const uint32_t*>(&lo2);
+                for (int h = 0; h < 2; ++h) {                 // 16 keys: hi pieces in 8 columns, lo pieces in the next 8
+                    const float4 mm = lds4(mt + c + 16 * h);
+                    const float f = plain ? qs * mm.x : 1.f, a = plain ? mm.y - sub : -sub;
+                    uint32_t w[16];
+                    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float2 y = __ffma2_rn(make_float2(__uint_as_float(v[16 * h + 2 * e]), __uint_as_float(v[16 * h + 2 * e + 1])),
+                                              make_float2(f, f), make_float2(a, a));
+                        y.x = att_ex2(y.x);
+                        y.y = att_ex2(y.y);
+                        s = __fadd2_rn(s, y);
+                        const __half2 hi2 = __floats2half2_rn(y.x, y.y);
+                        const float2 hf = __half22float2(hi2);
+                        const __half2 lo2 = __floats2half2_rn(y.x - hf.x, y.y - hf.y);
+                        w[e] = *reinterpret_cast<const uint32_t*>(&hi2);
+                        w[8 + e] = *reinterpret_cast<const uint32_t*>(&lo2);
+                    }
+                    t_st16(ts + c + 16 * h, w);
+                    // (a page that no visible key lies on may have a NaN scale)
+                    const float z = s.x + s.y;
+                    if (!(z == 0.f)) l = fmaf(z, mm.z, l);
                 }
-                const float t0 = s0.x + s0.y, t1 = s1.x + s1.y;
-                // (a page that no visible key lies on may have a NaN scale)
-                if (!(t0 == 0.f)) l = fmaf(t0, m0.z, l);
-                if (!(t1 == 0.f)) l = fmaf(t1, m1.z, l);
-                t_st32(ts + c, w);                            // hi of 32 keys, then lo
-            }
+            });
             // O, which PV(j) adds to: rescaled if a reference was raised,
             // taken out if PV(j) begins it anew
             const bool flush = j > 0 && j % F::G == 0;
@@ -402,31 +468,34 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
                 const bool more = j > F::G;                   // there is a sum from earlier flushes
                 const float gs = sref == -INFINITY ? 0.f : att_ex2(sref - ref);
                 if (flush) sref = ref;
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t v[32];
-                    t_ld32(trow + F::T_O + c, v);
-                    if (!flush) {
+                if (!flush) {
+                    t_each32<D>(trow + F::T_O, [&](int c, uint32_t (&v)[32]) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
                         t_st32(trow + F::T_O + c, v);
-                    } else if (F::SUM_SMEM) {
+                    });
+                } else if (F::SUM_SMEM) {
+                    t_each32<D>(trow + F::T_O, [&](int c, uint32_t (&v)[32]) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
                             const uint32_t a = sum + (c + e) * (PF_ROWS * 4);
                             const float o = __uint_as_float(v[e]) * f;
                             pf_sts(a, more ? fmaf(pf_lds(a), gs, o) : o);
                         }
-                    } else if (rok) {
+                    });
+                } else {
+                    t_each32<D>(trow + F::T_O, [&](int c, uint32_t (&v)[32]) {
+                        if (rok) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            float4 o = make_float4(__uint_as_float(v[e]) * f, __uint_as_float(v[e + 1]) * f,
-                                                   __uint_as_float(v[e + 2]) * f, __uint_as_float(v[e + 3]) * f);
-                            if (more) o = pf_fma4(pf_ld4(yrow + c + e, ovec), gs, o);
-                            pf_st4(yrow + c + e, o, ovec);
+                            for (int e = 0; e < 32; e += 4) {
+                                float4 o = make_float4(__uint_as_float(v[e]) * f, __uint_as_float(v[e + 1]) * f,
+                                                       __uint_as_float(v[e + 2]) * f, __uint_as_float(v[e + 3]) * f);
+                                if (more) o = pf_fma4(pf_ld4(yrow + c + e, ovec), gs, o);
+                                pf_st4(yrow + c + e, o, ovec);
+                            }
                         }
-                    }
-                    __syncwarp();
+                        __syncwarp();
+                    });
                 }
             }
             t_wait_st();
@@ -451,30 +520,49 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
                 const float gs = sref == -INFINITY ? 0.f : att_ex2(sref - ref);
                 const bool more = nt > F::G;
                 const float f = l == 0.f ? 0.f : att_pow2(e0) / l;
+                // through shared memory (the K and V buffers, free by now), so
+                // that a warp stores whole rows
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t v[32];
                     t_ld32(trow + F::T_O + c, v);
-                    if (rok) {
+                    t_wait32(v);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            float4 o = make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), __uint_as_float(v[e + 2]),
-                                                   __uint_as_float(v[e + 3]));
-                            if (more) {
-                                float4 z;
-                                if (F::SUM_SMEM) {
-                                    const uint32_t a = sum + (c + e) * (PF_ROWS * 4);
-                                    z = make_float4(pf_lds(a), pf_lds(a + PF_ROWS * 4), pf_lds(a + 2 * PF_ROWS * 4), pf_lds(a + 3 * PF_ROWS * 4));
-                                } else {
-                                    z = pf_ld4(yrow + c + e, ovec);
-                                }
-                                o = pf_fma4(z, gs, o);
+                    for (int e = 0; e < 32; e += 4) {
+                        float4 o = make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), __uint_as_float(v[e + 2]),
+                                               __uint_as_float(v[e + 3]));
+                        if (more) {
+                            float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (F::SUM_SMEM) {
+                                const uint32_t a = sum + (c + e) * (PF_ROWS * 4);
+                                z = make_float4(pf_lds(a), pf_lds(a + PF_ROWS * 4), pf_lds(a + 2 * PF_ROWS * 4), pf_lds(a + 3 * PF_ROWS * 4));
+                            } else if (rok) {
+                                z = pf_ld4(yrow + c + e, ovec);
                             }
-                            pf_st4(yrow + c + e, l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * f, o.y * f, o.z * f, o.w * f),
-                                   ovec);
+                            o = pf_fma4(z, gs, o);
                         }
+                        if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
+                        const uint32_t a = sbase + r * (D * 4) + ((((c + e) >> 2) ^ (r & 7)) << 4);
+                        sts128(a, __float_as_uint(o.x * f), __float_as_uint(o.y * f), __float_as_uint(o.z * f), __float_as_uint(o.w * f));
                     }
-                    __syncwarp();
+                }
+            }
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(PF_SOFT * 32) : "memory");
+        if (ok) {
+            constexpr int RW = D == 64 ? 2 : 1, NP = D == 256 ? 2 : 1, NR = PF_ROWS / PF_SOFT;
+            int hl;                                           // lane x: row x of this warp
+            const int64_t rl = row_of(min(warp * NR + (lane & (NR - 1)), rows - 1), hl);
+            const uint64_t prow = reinterpret_cast<uint64_t>(P.out + rl * P.ld_out + (int64_t)hl * D);
+#pragma unroll 4
+            for (int y = 0; y < NR; y += RW) {
+                const int z = y + (D == 64 ? lane >> 4 : 0), w = warp * NR + z;
+                float* o = reinterpret_cast<float*>(__shfl_sync(0xFFFFFFFFu, prow, z));
+#pragma unroll
+                for (int h = 0; h < NP; ++h) {
+                    const int pc = 32 * h + (D == 64 ? lane & 15 : lane);
+                    const float4 x = lds4(sbase + w * (D * 4) + ((pc ^ (w & 7)) << 4));
+                    if (w < rows) pf_st4(o + 4 * pc, x, ovec);
                 }
             }
         }
@@ -540,6 +628,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
             const int b = j & 1;
             const uint32_t ph = (uint32_t)(j >> 1) & 1;
             if (j >= 2 && !(ok = pf_wait(&k_free[b], ph ^ 1, P.timeout_ns))) break;
+            if (j == 1 && !(ok = pf_wait(&q_full, 0, P.timeout_ns))) break;     // q's pieces have left the second buffers
             bool vzero[GPW];
 #pragma unroll
             for (int x = 0; x < GPW; ++x) {
@@ -587,7 +676,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
         const uint64_t qd = pf_desc(sbase + F::Q_OFF, F::SBO_K);
         auto mma_s = [&](int j) -> bool {
             const int b = j & 1;
-            if (!mbar_wait_bounded(&k_full[b], (uint32_t)(j >> 1) & 1, P.timeout_ns)) return false;
+            if (!att_wait(&k_full[b], (uint32_t)(j >> 1) & 1, P.timeout_ns)) return false;
             t_after();
             const uint32_t d = tmem + F::T_S + b * NK;
             const uint64_t kb = kd + (b * F::KB >> 4);
@@ -603,13 +692,13 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
             pf_commit(&k_free[b]);
             return true;
         };
-        ok = mbar_wait_bounded(&q_full, 0, P.timeout_ns);
+        ok = att_wait(&q_full, 0, P.timeout_ns);
         t_after();
         ok = ok && mma_s(0) && (nt < 2 || mma_s(1));
         for (int j = 0; ok && j < nt; ++j) {
             const int b = j & 1;
-            ok = mbar_wait_bounded(&p_full[b], (uint32_t)(j >> 1) & 1, P.timeout_ns) &&
-                 mbar_wait_bounded(&v_full[b], (uint32_t)(j >> 1) & 1, P.timeout_ns);
+            ok = att_wait(&p_full[b], (uint32_t)(j >> 1) & 1, P.timeout_ns) &&
+                 att_wait(&v_full[b], (uint32_t)(j >> 1) & 1, P.timeout_ns);
             if (!ok) break;
             t_after();
             const uint32_t a = tmem + F::T_S + b * NK;
@@ -618,13 +707,13 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
             for (int h = 1; h >= 0; --h)                      // lo pieces, hi pieces
 #pragma unroll
                 for (int i = 0; i < NK / 16; ++i)
-                    pf_mma_ts(tmem + F::T_O, a + 32 * (i >> 1) + 8 * (i & 1) + 16 * h, vb + 16 * i, pf_idesc(D),
+                    pf_mma_ts(tmem + F::T_O, a + 16 * i + 8 * h, vb + 16 * i, pf_idesc(D),
                               h == 0 || i > 0 || j % F::G != 0);
             pf_commit(&v_free[b]);
             pf_commit(&pv_done);
             if (j == nt - 1) pf_commit(&o_done);
             // S(j + 2) is written over the weights that PV(j) reads
-            if (j + 2 < nt) ok = mbar_wait_bounded(&pv_done, (uint32_t)j & 1, P.timeout_ns) && mma_s(j + 2);
+            if (j + 2 < nt) ok = att_wait(&pv_done, (uint32_t)j & 1, P.timeout_ns) && mma_s(j + 2);
         }
     }
     if (!ok && lane == 0) record_status(P.status, STATUS_TIMEOUT);
@@ -634,7 +723,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
             // (q_full's first phase has long been used: the rest of a second one)
             for (int i = 1; i < PF_SOFT; ++i) mbar_arrive(&q_full);
             pf_commit(&q_full);
-            if (!mbar_wait_bounded(&q_full, 1, drain_bound(P.timeout_ns))) record_status(P.status, STATUS_TIMEOUT);
+            if (!att_wait(&q_full, 1, drain_bound(P.timeout_ns))) record_status(P.status, STATUS_TIMEOUT);
         }
         __syncwarp();
     }
