@@ -31,15 +31,16 @@
 //
 // Rounding.  The tensor cores truncate when they add to an accumulator, which
 // over thousands of keys shrinks O by 2e-8 per MMA (7e-6 after 3000 keys).  So O
-// starts anew every G tiles (32 MMAs), and the softmax threads add it up in
+// starts anew every G tiles (64 MMAs; error 1e-6, at 5 % of the time), and the softmax threads add it up in
 // fp32: in shared memory, or for D = 256, where there is no room, in the output
 // rows.
 //
 // Warps.  0-7 softmax, 8-11 converters: each takes the codes of 16-key groups
 // (one page each) of a tile from global memory through registers, a tile
-// ahead, into fp16 in the MMA's core-matrix layout; 12 issues the MMAs.
-// Tensor order: PV(j), S(j + 2), PV(j + 1), ...: while PV(j) and S(j + 2) run the
-// softmax works on tile j + 1.
+// ahead, into fp16 in the MMA's core-matrix layout; 12 issues S, 13 PV
+// (one thread for both spent as long on waits and commits as on the MMAs).
+// While PV(j) and then S(j + 2), which takes its place, run, the softmax works
+// on tile j + 1.
 //
 // Every wait is bounded: on a timeout a role records it and leaves its loop;
 // the MMAs in flight end (bounded) before the tensor memory is freed.
@@ -50,54 +51,61 @@ namespace {
 
 constexpr int PF_ROWS = 128;
 constexpr int PF_SOFT = 8, PF_CONV = 4;                      // softmax, converter warps
-constexpr int PF_MMA_WARP = PF_SOFT + PF_CONV;
-constexpr int PF_THREADS = (PF_MMA_WARP + 1) * 32;
+constexpr int PF_MMA_WARP = PF_SOFT + PF_CONV;               // issues S; the next one issues PV
+constexpr int PF_THREADS = (PF_MMA_WARP + 2) * 32;
 // Weights are 2^(u - ref + 11), at most 2^15: the lo pieces' floor of 2^-25 is
 // 2^-36 of the row's largest weight or less.
-constexpr float PF_SHIFT = 11.f;
-constexpr float PF_RAISE = 4.f;
+constexpr float PF_SHIFT = 8.f;
+constexpr float PF_RAISE = 7.f;
+constexpr int PF_NK = 128, PF_G = 4;
 
 template <int D>
 struct Pf {
-    static constexpr int NK = D == 256 ? 64 : 128;           // keys of a tile
+    static constexpr int NK = D == 256 ? 64 : PF_NK;         // keys of a tile
+    static constexpr int NB = D == 256 ? 2 : 256 / PF_NK;              // tiles in flight: S buffers, K and V stages
     static constexpr int NG = NK / 16;                       // 16-key groups
     static constexpr int GPW = NG / PF_CONV;                 // groups of a converter warp
-    static constexpr int G = D == 256 ? 4 : 2;               // tiles between two flushes of O (even: warps 0-3 do them)
+    static constexpr int G = D == 256 ? 8 : PF_G;                              // tiles between two flushes of O (even: warps 0-3 do them)
     static constexpr bool QLO_SMEM = D == 256;
     static constexpr uint32_t KB = NK * D * 2;               // bytes of a K or V tile
-    static constexpr uint32_t K_OFF = 0, V_OFF = 2 * KB, Q_OFF = 4 * KB;
+    static constexpr uint32_t K_OFF = 0, V_OFF = NB * KB, Q_OFF = 2 * NB * KB;
     static constexpr bool SUM_SMEM = D <= 128;               // where flushed O goes: [D][rows] fp32, or the output
     static constexpr uint32_t SUM_OFF = Q_OFF + (QLO_SMEM ? PF_ROWS * D * 2 : 0);
     static constexpr uint32_t META_OFF = SUM_OFF + (SUM_SMEM ? PF_ROWS * D * 4 : 0);
-    // (ks, log2, 1 / rel) of the groups of 4 tiles; and one CTA per SM, as each takes all of the tensor memory
-    static constexpr uint32_t SMEM = META_OFF + 4 * NG * 16 > 120 * 1024 ? META_OFF + 4 * NG * 16 : 120 * 1024;
+    // (ks, log2, 1 / rel) of the groups of 8 tiles; and one CTA per SM, as each takes all of the tensor memory
+    static constexpr uint32_t SMEM = META_OFF + 8 * NG * 16 > 120 * 1024 ? META_OFF + 8 * NG * 16 : 120 * 1024;
     // tensor memory columns
-    static constexpr uint32_t T_S = 0, T_O = 2 * NK, T_QH = T_O + D, T_QL = T_QH + D / 2;
+    static constexpr uint32_t T_S = 0, T_O = NB * NK, T_QH = T_O + D, T_QL = T_QH + D / 2;
     static_assert(T_QH + (QLO_SMEM ? D / 2 : D) <= 512, "tensor memory");
-    // q's pieces on their way: hi of row w in the second K buffer, lo in the second V buffer; D = 256: hi in both
+    // q's pieces on their way: hi of row w in the last two K stages, lo in the last two V stages; D = 256: hi in the last
+    // K and the last V stage
+    static constexpr int Q_STAGE = D == 256 || NB == 2 ? 1 : NB - 2;    // the first of them
     __device__ static constexpr uint32_t stage_hi(int w) {
-        return D == 256 && w >= 64 ? V_OFF + KB + (w - 64) * D * 2 : K_OFF + KB + w * D * 2;
+        return D == 256 && w >= 64 ? V_OFF + KB + (w - 64) * D * 2 : K_OFF + Q_STAGE * KB + w * D * 2;
     }
-    __device__ static constexpr uint32_t stage_lo(int w) { return V_OFF + KB + w * D * 2; }
+    __device__ static constexpr uint32_t stage_lo(int w) { return V_OFF + Q_STAGE * KB + w * D * 2; }
     static constexpr uint32_t SBO_K = 16 * D, SBO_V = 16 * NK;    // core matrices of 8 rows; 128 bytes along K
 };
 
-__device__ __forceinline__ uint64_t pf_desc(uint32_t addr, uint32_t sbo) {
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)(128 >> 4) << 16 | (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 |
-           (uint64_t)1 << 46;                                // no swizzle, this architecture's descriptor version
-}
+// A shared-memory descriptor's words: start address and 128 bytes between core
+// matrices along K; `sbo` bytes along the rows, this architecture's version, no
+// swizzle.
+__device__ __forceinline__ uint32_t pf_desc_lo(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | (128u >> 4) << 16; }
+__host__ __device__ constexpr uint32_t pf_desc_hi(uint32_t sbo) { return (sbo >> 4) | 1u << 14; }
 __host__ __device__ constexpr uint32_t pf_idesc(int n) {     // fp16 A and B, K-major, fp32 accumulators, M = 128
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
-__device__ __forceinline__ void pf_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(idesc), "r"(acc));
+// D (tensor memory) = A . B (+ D if acc).  Descriptors come as their low words:
+// one register to prepare per operand (see pf_desc_lo).
+__device__ __forceinline__ void pf_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t bhi, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 bd;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 bd, {%2, %3};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %4, p;\n\t}" ::"r"(d),
+                 "r"(a), "r"(b), "r"(bhi), "r"(idesc), "r"(acc));
 }
-__device__ __forceinline__ void pf_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(acc));
+__device__ __forceinline__ void pf_mma_ss(uint32_t d, uint32_t a, uint32_t ahi, uint32_t b, uint32_t bhi, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 ad, {%1, %2};\n\tmov.b64 bd, {%3, %4};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %5, p;\n\t}" ::"r"(d),
+                 "r"(a), "r"(ahi), "r"(b), "r"(bhi), "r"(idesc), "r"(acc));
 }
 __device__ __forceinline__ void pf_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -175,9 +183,6 @@ __device__ __forceinline__ float pf_lds(uint32_t a) {
     return v;
 }
 __device__ __forceinline__ void pf_sts(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
-__device__ __forceinline__ float4 pf_ld4(const float* y, bool vec) {
-    return vec ? *reinterpret_cast<const float4*>(y) : make_float4(y[0], y[1], y[2], y[3]);
-}
 __device__ __forceinline__ void pf_st4(float* y, float4 o, bool vec) {
     if (vec) {
         *reinterpret_cast<float4*>(y) = o;
@@ -203,9 +208,9 @@ __device__ __forceinline__ bool pf_wait(uint64_t* bar, uint32_t parity, uint64_t
 template <int D, bool EXTRA>
 __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid_constant__ AttnParams P) {
     using F = Pf<D>;
-    constexpr int NK = F::NK, NG = F::NG;
+    constexpr int NK = F::NK, NG = F::NG, NB = F::NB;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], pv_done, q_full, o_done;
+    __shared__ uint64_t k_full[F::NB], k_free[F::NB], v_full[F::NB], v_free[F::NB], s_full[F::NB], p_full[F::NB], q_full, o_done;
     __shared__ uint64_t ref_full[4], fin[4];                 // per warp of rows: a tile's reference is out; the odd tiles are done
     __shared__ float refs[PF_ROWS], lodd[PF_ROWS], lrodd[PF_ROWS], qscale[PF_ROWS];
     __shared__ uint32_t tslot;
@@ -251,7 +256,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
     const int e0 = pe >= 0 ? att_e0(__ldg(P.c.vs + (int64_t)pe * P.c.n_kv + hk)) : 0;
 
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < F::NB; ++i) {
             mbar_init(&k_full[i], PF_CONV);
             mbar_init(&v_full[i], PF_CONV);
             mbar_init(&k_free[i], 1);
@@ -263,7 +268,6 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
             mbar_init(&ref_full[i], 1);
             mbar_init(&fin[i], 1);
         }
-        mbar_init(&pv_done, 1);
         mbar_init(&o_done, 1);
         mbar_init(&q_full, PF_SOFT);
         fence_mbar_init();
@@ -275,8 +279,11 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
     t_before();
     __syncthreads();
     t_after();
-    const uint32_t tmem = tslot, sbase = smem_u32(smem), meta = sbase + F::META_OFF;
-    bool ok = true;
+    // (all of the tensor memory: it begins at column 0, and as a literal the
+    // MMAs' addresses need no preparation)
+    constexpr uint32_t tmem = 0;
+    bool ok = tslot == 0;
+    const uint32_t sbase = smem_u32(smem), meta = sbase + F::META_OFF;
 
     if (warp < PF_SOFT) {
         // ---- softmax: thread = row, warps 0-3 even tiles, 4-7 odd ones
@@ -292,7 +299,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
         const float slope = EXTRA && P.slopes ? __ldg(P.slopes + head) : 0.f;
         const uint32_t trow = tmem + ((uint32_t)(w4 * 32) << 16);
         // q: whole rows by a warp (lanes along the dims), their pieces through
-        // shared memory (the second K and V buffers, free until q_full) to
+        // shared memory (the last K and V stages, free until q_full) to
         // the rows' threads, and on to tensor memory.  16-byte pieces of a row
         // are swizzled by the row.
         {
@@ -367,10 +374,18 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
         float* const yrow = P.out + qrow * P.ld_out + (int64_t)head * D;
         const bool ovec = ((reinterpret_cast<uintptr_t>(P.out) | (uintptr_t)(P.ld_out * 4)) & 15) == 0;
         const uint32_t sum = sbase + F::SUM_OFF + r * 4;
+        // Where this row's flushed column c + e lies in the output rows: 32 x 32
+        // blocks transposed, so that a warp's access is one line (rows of an
+        // incomplete block: in place).
+        const bool block = w4 * 32 + 32 <= rows;
+        auto out_slot = [&](int c, int e) -> float* {
+            const uint64_t y = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(yrow), e);
+            return block ? reinterpret_cast<float*>(y) + c + lane : yrow + c + e;
+        };
         for (int j = wg; j < nt; j += 2) {
             const int k0 = key0(j);
-            const uint32_t ts = trow + F::T_S + wg * NK, mt = meta + (j & 3) * NG * 16;
-            if (!(ok = pf_wait(&s_full[wg], (uint32_t)(j >> 1) & 1, P.timeout_ns))) break;
+            const uint32_t ts = trow + F::T_S + (j % NB) * NK, mt = meta + (j & 7) * NG * 16;
+            if (!(ok = pf_wait(&s_full[j % NB], (uint32_t)(j / NB) & 1, P.timeout_ns))) break;
             t_after();
             const bool whole = k0 + NK <= vpre || (k0 >= vlo && k0 + NK <= vhi);
             const bool plain = !EXTRA && __all_sync(0xFFFFFFFFu, whole);
@@ -462,7 +477,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
             // taken out if PV(j) begins it anew
             const bool flush = j > 0 && j % F::G == 0;
             if (j > 0 && (flush || __any_sync(0xFFFFFFFFu, raise))) {
-                if (!(ok = pf_wait(&pv_done, (uint32_t)(j - 1) & 1, P.timeout_ns))) break;
+                if (!(ok = pf_wait(&v_free[(j - 1) % NB], (uint32_t)((j - 1) / NB) & 1, P.timeout_ns))) break;
                 t_after();
                 const float f = raise ? (before == -INFINITY ? 0.f : att_ex2(before - ref)) : 1.f;
                 const bool more = j > F::G;                   // there is a sum from earlier flushes
@@ -476,32 +491,38 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
                     });
                 } else if (F::SUM_SMEM) {
                     t_each32<D>(trow + F::T_O, [&](int c, uint32_t (&v)[32]) {
+                        // (all loads before the first store: they could not pass it)
+                        float z[32];
+                        if (more) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const uint32_t a = sum + (c + e) * (PF_ROWS * 4);
-                            const float o = __uint_as_float(v[e]) * f;
-                            pf_sts(a, more ? fmaf(pf_lds(a), gs, o) : o);
+                            for (int e = 0; e < 32; ++e) z[e] = pf_lds(sum + (c + e) * (PF_ROWS * 4)) * gs;
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) z[e] = 0.f;
                         }
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) pf_sts(sum + (c + e) * (PF_ROWS * 4), fmaf(__uint_as_float(v[e]), f, z[e]));
                     });
                 } else {
                     t_each32<D>(trow + F::T_O, [&](int c, uint32_t (&v)[32]) {
-                        if (rok) {
+                        float z[32];
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                float4 o = make_float4(__uint_as_float(v[e]) * f, __uint_as_float(v[e + 1]) * f,
-                                                       __uint_as_float(v[e + 2]) * f, __uint_as_float(v[e + 3]) * f);
-                                if (more) o = pf_fma4(pf_ld4(yrow + c + e, ovec), gs, o);
-                                pf_st4(yrow + c + e, o, ovec);
-                            }
+                        for (int e = 0; e < 32; ++e) {
+                            const float* y = out_slot(c, e);
+                            z[e] = more && rok ? *(const volatile float*)y * gs : 0.f;
                         }
-                        __syncwarp();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            float* y = out_slot(c, e);
+                            if (rok) *(volatile float*)y = fmaf(__uint_as_float(v[e]), f, z[e]);
+                        }
                     });
                 }
             }
             t_wait_st();
             t_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[wg]);
+            if (lane == 0) mbar_arrive(&p_full[j % NB]);
         }
         if (wg == 1) {
             *(volatile float*)&lodd[r] = l;
@@ -510,7 +531,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
             if (lane == 0) mbar_arrive(&fin[w4]);
         } else {
             // ---- output.  (The last PV has a barrier of its own: which phase
-            // pv_done is in by now is not known, and a parity does not tell.)
+            // v_free is in by now is not known, and a parity does not tell.)
             ok = ok && pf_wait(&fin[w4], 0, P.timeout_ns) && pf_wait(&o_done, 0, P.timeout_ns);
             if (ok) {
                 t_after();
@@ -532,12 +553,13 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
                         float4 o = make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), __uint_as_float(v[e + 2]),
                                                __uint_as_float(v[e + 3]));
                         if (more) {
-                            float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+                            float4 z;
                             if (F::SUM_SMEM) {
                                 const uint32_t a = sum + (c + e) * (PF_ROWS * 4);
                                 z = make_float4(pf_lds(a), pf_lds(a + PF_ROWS * 4), pf_lds(a + 2 * PF_ROWS * 4), pf_lds(a + 3 * PF_ROWS * 4));
-                            } else if (rok) {
-                                z = pf_ld4(yrow + c + e, ovec);
+                            } else {
+                                const float *y0 = out_slot(c, e), *y1 = out_slot(c, e + 1), *y2 = out_slot(c, e + 2), *y3 = out_slot(c, e + 3);
+                                z = rok ? make_float4(*y0, *y1, *y2, *y3) : make_float4(0.f, 0.f, 0.f, 0.f);
                             }
                             o = pf_fma4(z, gs, o);
                         }
@@ -625,17 +647,17 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
 #pragma unroll
         for (int x = 0; x < GPW; ++x) pnext[x] = page(1, g0 + x);
         for (int j = 0; j < nt; ++j) {
-            const int b = j & 1;
-            const uint32_t ph = (uint32_t)(j >> 1) & 1;
-            if (j >= 2 && !(ok = pf_wait(&k_free[b], ph ^ 1, P.timeout_ns))) break;
-            if (j == 1 && !(ok = pf_wait(&q_full, 0, P.timeout_ns))) break;     // q's pieces have left the second buffers
+            const int b = j % NB;
+            const uint32_t ph = (uint32_t)(j / NB) & 1;
+            if (j >= NB && !(ok = pf_wait(&k_free[b], ph ^ 1, P.timeout_ns))) break;
+            if (j == F::Q_STAGE && !(ok = pf_wait(&q_full, 0, P.timeout_ns))) break;     // q's pieces have left the stages
             bool vzero[GPW];
 #pragma unroll
             for (int x = 0; x < GPW; ++x) {
                 const int g = g0 + x, k0 = key0(j) + 16 * g;
                 const float rel = att_rel(vs[x] * is, vzero[x]);
                 if (lane == 0) {
-                    sts128(meta + ((j & 3) * NG + g) * 16, __float_as_uint(ks[x]), __float_as_uint(pg[x] < 0 ? -INFINITY : att_lg2(rel)),
+                    sts128(meta + ((j & 7) * NG + g) * 16, __float_as_uint(ks[x]), __float_as_uint(pg[x] < 0 ? -INFINITY : att_lg2(rel)),
                            __float_as_uint(att_rcp(rel)), 0u);
                     if (pg[x] < 0 && k0 < hi) {               // keys without a page: does a row see one of them?
                         const int a = max(k0, lo), e = min(k0 + 16, hi);
@@ -654,7 +676,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
                 for (int x = 0; x < GPW; ++x) pg[x] = pnext[x];
                 load_k(j + 1);
             }
-            if (j >= 2 && !(ok = pf_wait(&v_free[b], ph ^ 1, P.timeout_ns))) break;
+            if (j >= NB && !(ok = pf_wait(&v_free[b], ph ^ 1, P.timeout_ns))) break;
 #pragma unroll
             for (int x = 0; x < GPW; ++x) {
                 const uint32_t dst = sbase + F::V_OFF + b * F::KB + 2 * (g0 + x) * 128 + (lane >> 3) * F::SBO_V + (lane & 7) * 16;
@@ -670,58 +692,57 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
                 for (int x = 0; x < GPW; ++x) pnext[x] = page(j + 2, g0 + x);
             }
         }
-    } else if (lane == 0) {
-        // ---- MMA issue
-        const uint64_t kd = pf_desc(sbase + F::K_OFF, F::SBO_K), vd = pf_desc(sbase + F::V_OFF, F::SBO_V);
-        const uint64_t qd = pf_desc(sbase + F::Q_OFF, F::SBO_K);
-        auto mma_s = [&](int j) -> bool {
-            const int b = j & 1;
-            if (!att_wait(&k_full[b], (uint32_t)(j >> 1) & 1, P.timeout_ns)) return false;
+    } else if (warp == PF_MMA_WARP && lane == 0) {
+        // ---- issue of S
+        const uint32_t kd = pf_desc_lo(sbase + F::K_OFF), qd = pf_desc_lo(sbase + F::Q_OFF);
+        constexpr uint32_t khi = pf_desc_hi(F::SBO_K);
+        ok = att_wait(&q_full, 0, P.timeout_ns);
+        for (int j = 0; ok && j < nt; ++j) {
+            const int b = j % NB;
+            const uint32_t ph = (uint32_t)(j / NB) & 1;
+            // S(j) is written over the weights that PV(j - NB) read
+            if (j >= NB && !(ok = att_wait(&v_free[b], ph ^ 1, P.timeout_ns))) break;
+            if (!(ok = att_wait(&k_full[b], ph, P.timeout_ns))) break;
             t_after();
-            const uint32_t d = tmem + F::T_S + b * NK;
-            const uint64_t kb = kd + (b * F::KB >> 4);
+            const uint32_t d = tmem + F::T_S + b * NK, kb = kd + (b * F::KB >> 4);
             // (the lo pieces first: adding them to a large sum would truncate it once more each)
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
-                if (F::QLO_SMEM) pf_mma_ss(d, qd + 16 * i, kb + 16 * i, pf_idesc(NK), i > 0);
-                else pf_mma_ts(d, tmem + F::T_QL + 8 * i, kb + 16 * i, pf_idesc(NK), i > 0);
+                if (F::QLO_SMEM) pf_mma_ss(d, qd + 16 * i, khi, kb + 16 * i, khi, pf_idesc(NK), i > 0);
+                else pf_mma_ts(d, tmem + F::T_QL + 8 * i, kb + 16 * i, khi, pf_idesc(NK), i > 0);
             }
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) pf_mma_ts(d, tmem + F::T_QH + 8 * i, kb + 16 * i, pf_idesc(NK), 1);
+            for (int i = 0; i < D / 16; ++i) pf_mma_ts(d, tmem + F::T_QH + 8 * i, kb + 16 * i, khi, pf_idesc(NK), 1);
             pf_commit(&s_full[b]);
             pf_commit(&k_free[b]);
-            return true;
-        };
-        ok = att_wait(&q_full, 0, P.timeout_ns);
-        t_after();
-        ok = ok && mma_s(0) && (nt < 2 || mma_s(1));
-        for (int j = 0; ok && j < nt; ++j) {
-            const int b = j & 1;
-            ok = att_wait(&p_full[b], (uint32_t)(j >> 1) & 1, P.timeout_ns) &&
-                 att_wait(&v_full[b], (uint32_t)(j >> 1) & 1, P.timeout_ns);
-            if (!ok) break;
+        }
+    } else if (warp > PF_MMA_WARP && lane == 0) {
+        // ---- issue of PV
+        const uint32_t vd = pf_desc_lo(sbase + F::V_OFF);
+        constexpr uint32_t vhi = pf_desc_hi(F::SBO_V);
+        for (int j = 0; j < nt; ++j) {
+            const int b = j % NB;
+            const uint32_t ph = (uint32_t)(j / NB) & 1;
+            if (!(ok = att_wait(&v_full[b], ph, P.timeout_ns) && att_wait(&p_full[b], ph, P.timeout_ns))) break;
             t_after();
-            const uint32_t a = tmem + F::T_S + b * NK;
-            const uint64_t vb = vd + (b * F::KB >> 4);
+            const uint32_t a = tmem + F::T_S + b * NK, vb = vd + (b * F::KB >> 4);
 #pragma unroll
             for (int h = 1; h >= 0; --h)                      // lo pieces, hi pieces
 #pragma unroll
                 for (int i = 0; i < NK / 16; ++i)
-                    pf_mma_ts(tmem + F::T_O, a + 16 * i + 8 * h, vb + 16 * i, pf_idesc(D),
-                              h == 0 || i > 0 || j % F::G != 0);
+                    pf_mma_ts(tmem + F::T_O, a + 16 * i + 8 * h, vb + 16 * i, vhi, pf_idesc(D), h == 0 || i > 0 || j % F::G != 0);
             pf_commit(&v_free[b]);
-            pf_commit(&pv_done);
             if (j == nt - 1) pf_commit(&o_done);
-            // S(j + 2) is written over the weights that PV(j) reads
-            if (j + 2 < nt) ok = att_wait(&pv_done, (uint32_t)j & 1, P.timeout_ns) && mma_s(j + 2);
         }
     }
     if (!ok && lane == 0) record_status(P.status, STATUS_TIMEOUT);
-    if (warp == PF_MMA_WARP) {
-        // every MMA issued has ended before the tensor memory goes
+    if (warp >= PF_MMA_WARP) {
+        // every MMA issued has ended before the tensor memory goes (each
+        // issuing thread commits its own; q_full's first phase has long been
+        // used, these are the arrivals of a second one)
         if (lane == 0) {
-            // (q_full's first phase has long been used: the rest of a second one)
-            for (int i = 1; i < PF_SOFT; ++i) mbar_arrive(&q_full);
+            if (warp == PF_MMA_WARP)
+                for (int i = 2; i < PF_SOFT; ++i) mbar_arrive(&q_full);
             pf_commit(&q_full);
             if (!att_wait(&q_full, 1, drain_bound(P.timeout_ns))) record_status(P.status, STATUS_TIMEOUT);
         }
@@ -730,7 +751,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
     t_before();
     __syncthreads();
     t_after();
-    if (warp == PF_MMA_WARP) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    if (warp == PF_MMA_WARP) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tslot));
 }
 
 template <int D>
