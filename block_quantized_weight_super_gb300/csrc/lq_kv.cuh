@@ -40,20 +40,38 @@ __device__ __forceinline__ int kv_find(int nseq, int64_t x, Key key) {
     return lo;
 }
 
+// The same by a whole warp, 32 keys at a time: keys in global memory cost a
+// memory latency per step.
+template <class Key>
+__device__ __forceinline__ int kv_find_warp(int nseq, int64_t x, Key key) {
+    int lo = 0, n = nseq;
+    while (n > 1) {
+        const int step = (n + 31) >> 5, i = (threadIdx.x & 31) * step;
+        const unsigned le = __ballot_sync(0xFFFFFFFFu, i < n && (int64_t)key(lo + min(i, n - 1)) <= x);
+        const int b = 31 - __clz(le | 1u);
+        lo += b * step;
+        n = min(step, n - b * step);
+    }
+    return lo;
+}
+
 // x / s rounded to the nearest integer, ties to even, exactly, in
-// [-127, 127]; s > 0 finite, both already multiplied by kv_up(s), inv the
-// fp32 reciprocal of s.  x * inv is within 3 ulps of the quotient, so its
-// rounding is off by one at most, and only next to a half-integer h; there the
-// sign of x - h s decides, which the fused multiply-add gives exactly (h s has
-// at most 32 significant bits, and kv_up keeps it out of the subnormals).
-__device__ __forceinline__ int kv_round(float x, float s, float inv) {
-    const float r = fminf(fmaxf(x * inv, -127.f), 127.f);
-    float n = rintf(r);
-    const float up = fmaf(-(n + 0.5f), s, x), dn = fmaf(-(n - 0.5f), s, x);
-    const bool odd = ((int)n & 1) != 0;
-    if (up > 0.f || (up == 0.f && odd)) n += 1.f;
-    else if (dn < 0.f || (dn == 0.f && odd)) n -= 1.f;
-    return (int)fminf(fmaxf(n, -127.f), 127.f);
+// [-127, 127], as the low byte of the result; s > 0 finite, x and s already
+// multiplied by kv_up(s), inv the fp32 reciprocal of s.  x * inv is within 3
+// ulps of the quotient, so its rounding n is off by one at most, and only next
+// to a half-integer.  d = x - n s shows it: both terms are multiples of the
+// smaller of their last places and d is below 2^24 of those, so the fused
+// multiply-add is exact.  Adding 1.5 * 2^23 rounds and leaves n in the low bits
+// (conversion instructions run at a quarter of the rate).
+__device__ __forceinline__ uint32_t kv_round(float x, float s, float inv) {
+    const float magic = 12582912.f;
+    float t = fminf(fmaxf(x * inv, -127.f), 127.f) + magic;
+    const float n = t - magic, d = fmaf(-n, s, x), h = 0.5f * s;
+    if (fabsf(d) >= h) {
+        const bool odd = (__float_as_uint(t) & 1u) != 0;
+        if (fabsf(d) > h || odd) t = fminf(fmaxf(n + copysignf(1.f, d), -127.f), 127.f) + magic;
+    }
+    return __float_as_uint(t);
 }
 
 // Power of two that keeps the arithmetic of kv_round normal for tiny scales.

@@ -6,7 +6,7 @@
 namespace lq {
 namespace {
 
-constexpr int APP_THREADS = 256;
+constexpr int APP_FULL_THREADS = 512, APP_ANY_THREADS = 128;
 
 // Sequence s owns the work items [base(s), base(s + 1)), base(s) =
 // floor(cu[s] / page) + 2 s: at least as many as the pages its new tokens
@@ -17,18 +17,179 @@ __device__ __forceinline__ int64_t app_base(const KvStep& S, int pshift, int s) 
     return S.cu ? (int64_t)(__ldg(S.cu + s) >> pshift) + 2 * s : s;
 }
 
-// One page, kv head and K (blockIdx.z = 0) or V (1).  Two passes over the
-// page's new rows: the largest |x|, then the codes (the second read comes from
-// L2).  A thread makes 4 codes of adjacent dims (K) or of adjacent slots (V),
-// one 32-bit word of the cache; a word that also holds earlier codes keeps
-// or rescales them.
-__global__ void __launch_bounds__(APP_THREADS) kv8_append_kernel(const KvView C, const KvStep S, const float* k,
+// A page's new slots and where its rows, codes and scale lie.
+struct AppPage {
+    const float* x;          // row of slot s0, this head
+    int64_t ld;
+    int8_t* codes;
+    float* scale;
+    int s0, s1;              // new slots [s0, s1)
+};
+
+// The largest |x| of the block as bits (a NaN above all).
+template <int NT>
+__device__ __forceinline__ uint32_t app_max(uint32_t m, uint32_t* red) {
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+    __syncthreads();
+    for (int i = 0; i < NT / 32; ++i) m = max(m, red[i]);
+    return m;
+}
+// The scale that a maximum asks for.
+__device__ __forceinline__ float app_scale(uint32_t m) {
+    return m < 0x7F800000u ? __uint_as_float(m) * (1.f / 127.f) : __uint_as_float(0x7FC00000u);
+}
+
+// Any page: two passes over its new rows, the largest |x|, then the codes.  A
+// thread makes 4 codes of adjacent dims (K) or of adjacent slots (V), one
+// 32-bit word of the cache; a word that also holds earlier codes keeps or
+// rescales them.
+template <int NT>
+__device__ __forceinline__ void append_any(const AppPage& p, bool isv, int D, int pshift, uint32_t* red) {
+    const int tid = threadIdx.x, s0 = p.s0, s1 = p.s1;
+    const int64_t ld = p.ld;
+    const float* const x = p.x;
+    uint32_t m = 0;
+    for (int d = tid; d < D; d += NT)               // (D is 64, 128 or 256)
+        for (int s = 0; s < s1 - s0; ++s) m = max(m, kv_absbits(x[s * ld + d]));
+    m = app_max<NT>(m, red);
+    const float was = s0 > 0 ? *p.scale : 0.f;
+    const float mine = app_scale(m);
+    const float now = kv_absbits(was) >= kv_absbits(mine) ? was : mine;  // NaN stays
+    const bool good = kv_absbits(now) < 0x7F800000u && now > 0.f;
+    const bool again = s0 > 0 && good && now > was;                      // earlier codes get the new scale
+    __syncthreads();                                                     // every thread has read *scale
+    if (tid == 0) *p.scale = now;
+    const float up = kv_up(now), su = now * up, inv = 1.f / su;
+
+    // code of (slot, dim), given the code there now
+    auto code = [&](int slot, int d, int had) -> signed char {
+        if (slot >= s0 && slot < s1) return good ? (signed char)kv_round(x[(slot - s0) * ld + d] * up, su, inv) : 0;
+        if (slot < s0 && again) return (signed char)kv_round((float)had * was * up, su, inv);
+        return (signed char)had;
+    };
+    const int first = again ? 0 : s0;                                    // slots to rewrite: [first, s1)
+    if (!isv) {
+        const int dw = D / 4;                                            // words per slot
+        for (int w = first * dw + tid; w < s1 * dw; w += NT) {
+            const int slot = w / dw, d = 4 * (w % dw);
+            char4* q = reinterpret_cast<char4*>(p.codes) + w;
+            const char4 c = slot < s0 ? *q : make_char4(0, 0, 0, 0);
+            *q = make_char4(code(slot, d, c.x), code(slot, d + 1, c.y), code(slot, d + 2, c.z), code(slot, d + 3, c.w));
+        }
+    } else {
+        const int w0 = first / 4, nw = (s1 + 3) / 4 - w0;                // slot words to rewrite
+        for (int u = tid; u < nw * D; u += NT) {
+            const int d = u % D, slot = 4 * (w0 + u / D);
+            char4* q = reinterpret_cast<char4*>(p.codes + ((int64_t)d << pshift) + slot);
+            const char4 c = *q;
+            *q = make_char4(code(slot, d, c.x), code(slot + 1, d, c.y), code(slot + 2, d, c.z), code(slot + 3, d, c.w));
+        }
+    }
+}
+
+// A page filled from its first slot on, with 16-byte rows: read once, 16
+// tokens x 32 dims per warp and step, a thread 4 tokens x 4 dims.  K's codes go
+// out as 32-byte pieces of a token; V's, which lie with the tokens adjacent,
+// through shared memory (a row of dims per line, one word of padding: free of
+// bank conflicts) and out in 16-byte pieces of a dim.  Bound by the reads.
+// Pages of more than APP_ELEMS values are read twice, in slabs of slots.
+constexpr int APP_ELEMS = 16384;                             // values that the block holds in registers
+template <int D>
+__device__ __forceinline__ void append_full(const AppPage& p, bool isv, int pshift, uint32_t* red, uint32_t* tile) {
+    constexpr int DT = D / 32, TS = APP_ELEMS / D, NI = APP_ELEMS / (16 * APP_FULL_THREADS);   // dim tiles, slots of a slab, steps of a warp
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = p.s1;
+    const int dq = (lane & 7) * 4, tq = (lane >> 3) * 4, ts = min(TS, 1 << pshift);
+    float4 v[NI][4];
+    auto load = [&](int t0) {                                // slots t0 .. t0 + ts - 1
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int T = i * (APP_FULL_THREADS / 32) + warp, d = T % DT * 32 + dq, t = T / DT * 16 + tq;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v[i][k] = t + k < ts && t0 + t + k < n ? __ldg(reinterpret_cast<const float4*>(p.x + (int64_t)(t0 + t + k) * p.ld + d))
+                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    };
+    uint32_t m = 0;
+    for (int t0 = 0; t0 < n; t0 += TS) {
+        load(t0);
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                m = max(max(m, max(kv_absbits(v[i][k].x), kv_absbits(v[i][k].y))), max(kv_absbits(v[i][k].z), kv_absbits(v[i][k].w)));
+    }
+    const float now = app_scale(app_max<APP_FULL_THREADS>(m, red));
+    if (tid == 0) *p.scale = now;
+    const bool good = kv_absbits(now) < 0x7F800000u && now > 0.f;
+    const float up = kv_up(now), su = now * up, inv = 1.f / su;
+    auto code = [&](float x) -> uint32_t { return good ? kv_round(x * up, su, inv) : 0u; };
+    for (int t0 = 0; t0 < n; t0 += TS) {
+        if (n > TS) load(t0);                                // (one slab: still there)
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int T = i * (APP_FULL_THREADS / 32) + warp, d = T % DT * 32 + dq, t = T / DT * 16 + tq;
+            if (t >= ts) continue;
+            uint32_t w[4];                                   // codes of a token: 4 dims
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                w[k] = prmt(prmt(code(v[i][k].x), code(v[i][k].y), 0x0040u), prmt(code(v[i][k].z), code(v[i][k].w), 0x0040u), 0x5410u);
+            if (!isv) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (t0 + t + k < n) *reinterpret_cast<uint32_t*>(p.codes + (int64_t)(t0 + t + k) * D + d) = w[k];
+            } else {
+                // 4 x 4 transpose: codes of a dim, 4 tokens
+                const uint32_t a = prmt(w[0], w[1], 0x5140u), b = prmt(w[0], w[1], 0x7362u);
+                const uint32_t c = prmt(w[2], w[3], 0x5140u), e = prmt(w[2], w[3], 0x7362u);
+                uint32_t* o = tile + d * (ts / 4 + 1) + t / 4;
+                const int pitch = ts / 4 + 1;
+                o[0] = prmt(a, c, 0x5410u);
+                o[pitch] = prmt(a, c, 0x7632u);
+                o[2 * pitch] = prmt(b, e, 0x5410u);
+                o[3 * pitch] = prmt(b, e, 0x7632u);
+            }
+        }
+        if (isv) {
+            __syncthreads();
+            const int per = ts / 16;                         // 16-byte pieces of a dim
+            for (int u = tid; u < D * per; u += APP_FULL_THREADS) {
+                const int d = u / per, s = u % per * 16;
+                const uint32_t* o = tile + d * (ts / 4 + 1) + s / 4;
+                uint4* q = reinterpret_cast<uint4*>(p.codes + ((int64_t)d << pshift) + t0 + s);
+                uint4 z = make_uint4(o[0], o[1], o[2], o[3]);
+                const int left = n - t0 - s;                 // new slots from here on
+                if (left <= 0) continue;
+                if (left < 16) {                             // the rest of the piece stays
+                    const uint4 h = *q;
+                    auto mix = [&](uint32_t a, uint32_t b, int k) {      // bytes 4k .. of a where new
+                        const int c = min(max(left - 4 * k, 0), 4);
+                        const uint32_t msk = c == 4 ? 0xFFFFFFFFu : (1u << (8 * c)) - 1;
+                        return (a & msk) | (b & ~msk);
+                    };
+                    z = make_uint4(mix(z.x, h.x, 0), mix(z.y, h.y, 1), mix(z.z, h.z, 2), mix(z.w, h.w, 3));
+                }
+                *q = z;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// One page and kv head; K (blockIdx.z = 0) or V (1), or, in a grid of depth 1,
+// one after the other (finding the page costs three memory latencies).  FULL:
+// pages that take many new tokens are expected; without that path the kernel needs a third of
+// the registers and a decode step's many small blocks all run at once.
+template <int D, bool FULL>
+__global__ void __launch_bounds__(FULL ? APP_FULL_THREADS : APP_ANY_THREADS, FULL ? 2 : 8) kv8_append_kernel(const KvView C, const KvStep S, const float* k,
                                                                  int64_t ld_k, const float* v, int64_t ld_v,
                                                                  unsigned* status) {
-    __shared__ uint32_t red[APP_THREADS / 32];
+    constexpr int NT = FULL ? APP_FULL_THREADS : APP_ANY_THREADS;
+    __shared__ uint32_t red[NT / 32];
+    __shared__ uint32_t tile[FULL ? APP_ELEMS / 4 + D : 1];
     const int head = blockIdx.y, tid = threadIdx.x;
-    const bool isv = blockIdx.z != 0;
-    const int s = kv_find(S.nseq, blockIdx.x, [&](int i) { return app_base(S, C.pshift, i); });
+    const int s = kv_find_warp(S.nseq, blockIdx.x, [&](int i) { return app_base(S, C.pshift, i); });
     const int row0 = kv_cu(S, s), n = kv_cu(S, s + 1) - row0, start = S.start[s];
     const int64_t end = (int64_t)start + n;                              // one past the last position
     const int64_t p0 = max(start, 0);                                    // first stored position
@@ -40,51 +201,22 @@ __global__ void __launch_bounds__(APP_THREADS) kv8_append_kernel(const KvView C,
         if (tid == 0) record_status(status, STATUS_BADARG);
         return;
     }
-    const int s0 = (int)(a - (pj << C.pshift)), s1 = (int)(b - (pj << C.pshift));     // its new slots
-    const int64_t ld = isv ? ld_v : ld_k;
-    const float* x = (isv ? v : k) + (row0 + (a - start)) * ld + (int64_t)head * C.d;  // row of slot s0
     const int64_t ph = (int64_t)page * C.n_kv + head;
-    float* scale = (isv ? C.vs : C.ks) + ph;
-    int8_t* codes = (isv ? C.v : C.k) + ph * ((int64_t)C.d << C.pshift);
-
-    uint32_t m = 0;
-    for (int e = tid; e < (s1 - s0) * C.d; e += APP_THREADS) m = max(m, kv_absbits(x[(e / C.d) * ld + e % C.d]));
-    m = __reduce_max_sync(0xFFFFFFFFu, m);
-    if ((tid & 31) == 0) red[tid >> 5] = m;
-    __syncthreads();
-    for (int i = 0; i < APP_THREADS / 32; ++i) m = max(m, red[i]);
-    const float was = s0 > 0 ? *scale : 0.f;
-    const float mine = m < 0x7F800000u ? __uint_as_float(m) * (1.f / 127.f) : __uint_as_float(0x7FC00000u);
-    const float now = kv_absbits(was) >= kv_absbits(mine) ? was : mine;  // NaN stays
-    const bool good = kv_absbits(now) < 0x7F800000u && now > 0.f;
-    const bool again = s0 > 0 && good && now > was;                      // earlier codes get the new scale
-    __syncthreads();                                                     // every thread has read *scale
-    if (tid == 0) *scale = now;
-    const float up = kv_up(now), su = now * up, inv = 1.f / su;
-
-    // code of (slot, dim), given the code there now
-    auto code = [&](int slot, int d, int had) -> int {
-        if (slot >= s0 && slot < s1) return good ? kv_round(x[(slot - s0) * ld + d] * up, su, inv) : 0;
-        if (slot < s0 && again) return kv_round((float)had * was * up, su, inv);
-        return had;
-    };
-    const int first = again ? 0 : s0;                                    // slots to rewrite: [first, s1)
-    if (!isv) {
-        const int dw = C.d / 4;                                          // words per slot
-        for (int w = first * dw + tid; w < s1 * dw; w += APP_THREADS) {
-            const int slot = w / dw, d = 4 * (w % dw);
-            char4* p = reinterpret_cast<char4*>(codes) + w;
-            char4 c = slot < s0 ? *p : make_char4(0, 0, 0, 0);
-            *p = make_char4(code(slot, d, c.x), code(slot, d + 1, c.y), code(slot, d + 2, c.z), code(slot, d + 3, c.w));
-        }
-    } else {
-        const int w0 = first / 4, nw = (s1 + 3) / 4 - w0;                // slot words to rewrite
-        for (int u = tid; u < nw * C.d; u += APP_THREADS) {
-            const int d = u % C.d, slot = 4 * (w0 + u / C.d);
-            char4* p = reinterpret_cast<char4*>(codes + ((int64_t)d << C.pshift) + slot);
-            char4 c = *p;
-            *p = make_char4(code(slot, d, c.x), code(slot + 1, d, c.y), code(slot + 2, d, c.z), code(slot + 3, d, c.w));
-        }
+    AppPage p;
+    p.s0 = (int)(a - (pj << C.pshift));
+    p.s1 = (int)(b - (pj << C.pshift));
+#pragma unroll 1
+    for (int z = blockIdx.z; z < 2; z += gridDim.z) {
+        const bool isv = z != 0;
+        p.ld = isv ? ld_v : ld_k;
+        p.x = (isv ? v : k) + (row0 + (a - start)) * p.ld + (int64_t)head * D;
+        p.codes = (isv ? C.v : C.k) + ph * ((int64_t)D << C.pshift);
+        p.scale = (isv ? C.vs : C.ks) + ph;
+        const bool vec = ((reinterpret_cast<uintptr_t>(isv ? v : k) | (uintptr_t)(p.ld * 4)) & 15) == 0;
+        if constexpr (!FULL) append_any<NT>(p, isv, D, C.pshift, red);
+        else if (p.s0 == 0 && p.s1 >= 8 && vec) append_full<D>(p, isv, C.pshift, red, tile);
+        else append_any<NT>(p, isv, D, C.pshift, red);
+        __syncthreads();
     }
 }
 
@@ -122,7 +254,12 @@ __global__ void __launch_bounds__(256) kv8_copy_kernel(const __grid_constant__ K
 cudaError_t launch_kv8_append(const KvView& C, const KvStep& S, const float* k, int64_t ld_k, const float* v,
                               int64_t ld_v, unsigned* status, cudaStream_t st) {
     const int64_t items = S.cu ? (int64_t)(S.ntok >> C.pshift) + 2 * (int64_t)S.nseq : S.nseq;
-    kv8_append_kernel<<<dim3((unsigned)items, (unsigned)C.n_kv, 2), APP_THREADS, 0, st>>>(C, S, k, ld_k, v, ld_v, status);
+    const bool full = S.ntok >= 8 * (int64_t)S.nseq;
+    const dim3 grid((unsigned)items, (unsigned)C.n_kv, full && items * C.n_kv >= 512 ? 1 : 2);
+    auto kern = C.d == 64    ? (full ? kv8_append_kernel<64, true> : kv8_append_kernel<64, false>)
+                : C.d == 128 ? (full ? kv8_append_kernel<128, true> : kv8_append_kernel<128, false>)
+                             : (full ? kv8_append_kernel<256, true> : kv8_append_kernel<256, false>);
+    kern<<<grid, full ? APP_FULL_THREADS : APP_ANY_THREADS, 0, st>>>(C, S, k, ld_k, v, ld_v, status);
     return cudaGetLastError();
 }
 
