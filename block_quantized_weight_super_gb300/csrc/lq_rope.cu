@@ -1,12 +1,13 @@
 // lq_rope.cu -- rotary positions with one or several axes.
 //
 // Pair i of a token at position p of the pair's axis is rotated by p * freq[i].
-// The angle is taken in turns, p * (freq[i] / 2 pi) in fp64, and only its
-// fractional part in [-1/2, 1/2] goes to fp32: at p = 2^20 the reduction error
-// is below 2^-35 turns, where an fp32 product would have lost 2^-7.  sincospi
-// of twice that fraction is accurate to fp32 rounding.  Two fp64 products and
-// one rounding per (token, pair), shared by all heads, are small beside the
-// memory traffic (8 bytes per element), which bounds the kernel.
+// The angle is taken in turns: freq[i] / 2 pi modulo 1, formed in fp64, as a
+// 64-bit fixed-point fraction; its product with the integer p modulo 2^64 is
+// the angle modulo 1, exact but for 2^-64 p turns, whatever the position's size
+// (an fp32 product would have lost 2^-7 turns at p = 2^20).  sincospi of the top
+// 32 bits is accurate to fp32 rounding.  The fp64 arithmetic, which runs at a
+// sixty-fourth of the fp32 rate, is needed once per block and pair.  The
+// kernel is bound by the memory traffic, 8 bytes per element.
 #include "lq_internal.h"
 #include "lq_kv.cuh"
 
@@ -14,59 +15,91 @@ namespace lq {
 namespace {
 
 constexpr int ROPE_THREADS = 256;
-constexpr int ROPE_MAX_PAIRS = 512;
+constexpr int ROPE_TOK = 4;                                   // tokens of a block where there are many
 
-// One token (blockIdx.x) and a range of its heads (blockIdx.y).  The table of
-// (cos, sin) per pair lies in shared memory; V = 4: a thread rotates four
-// adjacent pairs with 16-byte accesses (ROPE_HALF, widths and addresses
-// multiples of four floats), V = 1: one pair.
-template <int V>
+// TOK tokens from blockIdx.x TOK on and a range of their heads (blockIdx.y).
+// The table of (cos, sin) per pair and token lies in shared memory; V = 4: a
+// thread rotates four adjacent pairs with 16-byte accesses (ROPE_HALF, widths
+// and addresses multiples of four floats), V = 1: one pair.
+template <int V, int TOK>
 __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeParams P) {
-    __shared__ float2 cs[ROPE_MAX_PAIRS];
-    const int t = blockIdx.x, half = P.rot / 2;
+    extern __shared__ float2 cs[];                            // [TOK][half]; then turns [half]
+    const int t0 = blockIdx.x * TOK, half = P.rot / 2, nt = min(TOK, P.ntok - t0);
+    uint64_t* const turns = reinterpret_cast<uint64_t*>(cs + TOK * half);
     for (int i = threadIdx.x; i < half; i += ROPE_THREADS) {
+        const double f = P.freq[i] * 0.15915494309189533577;
+        turns[i] = (uint64_t)((f - floor(f)) * 18446744073709551616.0);
+    }
+    __syncthreads();
+    for (int u = threadIdx.x; u < half * nt; u += ROPE_THREADS) {
+        const int i = TOK == 1 ? u : u % half, t = t0 + (TOK == 1 ? 0 : u / half);
         const int a = P.axis ? P.axis[i] : 0;
         float s = 0.f, c = 1.f;
         if (a < P.n_axes) {
-            const double turns = (double)P.pos[(int64_t)a * P.ntok + t] * (P.freq[i] * 0.15915494309189533577);
-            sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+            const uint64_t z = turns[i] * (uint64_t)(int64_t)P.pos[(int64_t)a * P.ntok + t];
+            sincospif((float)(int32_t)(z >> 32) * 4.656612873077393e-10f, &s, &c);      // half turns: 2^-31
         } else {
             record_status(P.status, STATUS_BADARG);
         }
-        cs[i] = make_float2(c, s);
+        cs[u] = make_float2(c, s);
     }
     __syncthreads();
     const int heads = P.n_q + P.n_k, h0 = (int)((int64_t)heads * blockIdx.y / gridDim.y),
               h1 = (int)((int64_t)heads * (blockIdx.y + 1) / gridDim.y);
     const int units = half / V, tail = (P.d - P.rot) / V, per = units + tail;   // work items of a head
-    for (int u = threadIdx.x; u < (h1 - h0) * per; u += ROPE_THREADS) {
-        const int h = h0 + u / per, i = u % per;
-        const float* x = h < P.n_q ? P.q + t * P.ld_q + (int64_t)h * P.d : P.k + t * P.ld_k + (int64_t)(h - P.n_q) * P.d;
-        float* y = h < P.n_q ? P.qo + t * P.ld_qo + (int64_t)h * P.d : P.ko + t * P.ld_ko + (int64_t)(h - P.n_q) * P.d;
-        if (V == 4) {
-            if (i < units) {
-                const float4 a = *reinterpret_cast<const float4*>(x + 4 * i);
-                const float4 b = *reinterpret_cast<const float4*>(x + half + 4 * i);
-                const float2 c0 = cs[4 * i], c1 = cs[4 * i + 1], c2 = cs[4 * i + 2], c3 = cs[4 * i + 3];
-                *reinterpret_cast<float4*>(y + 4 * i) = make_float4(a.x * c0.x - b.x * c0.y, a.y * c1.x - b.y * c1.y,
-                                                                    a.z * c2.x - b.z * c2.y, a.w * c3.x - b.w * c3.y);
-                *reinterpret_cast<float4*>(y + half + 4 * i) =
-                    make_float4(b.x * c0.x + a.x * c0.y, b.y * c1.x + a.y * c1.y, b.z * c2.x + a.z * c2.y,
-                                b.w * c3.x + a.w * c3.y);
+    const int all = (h1 - h0) * per;
+    // K items at a time, their loads before the first store (which the
+    // compiler could not move past it: the rows may be rotated in place)
+    constexpr int K = V == 4 && TOK > 1 ? 3 : 1;
+    for (int w0 = threadIdx.x; w0 < all * nt; w0 += K * ROPE_THREADS) {
+        float4 a[K], b[K];
+        float* y[K];
+        int ci[K], kind[K];                                   // place in the table; 0: none, 1: rotated, 2: copied
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int w = w0 + k * ROPE_THREADS;
+            kind[k] = 0;
+            if (w >= all * nt) continue;
+            const int z = TOK == 1 ? 0 : w / all, u = TOK == 1 ? w : w % all;
+            const int h = h0 + u / per, i = u % per;
+            const int64_t t = t0 + z;
+            const bool isq = h < P.n_q;
+            const int64_t col = (int64_t)(isq ? h : h - P.n_q) * P.d;
+            const float* x = (isq ? P.q + t * P.ld_q : P.k + t * P.ld_k) + col;
+            y[k] = (isq ? P.qo + t * P.ld_qo : P.ko + t * P.ld_ko) + col;
+            kind[k] = i < units ? 1 : 2;
+            ci[k] = z * half + V * i;
+            const int ia = i >= units ? P.rot + V * (i - units) : V == 1 && P.adjacent ? 2 * i : V * i;
+            y[k] += ia;
+            if (V == 4) {
+                a[k] = *reinterpret_cast<const float4*>(x + ia);
+                if (i < units) b[k] = *reinterpret_cast<const float4*>(x + ia + half);
             } else {
-                const int e = P.rot + 4 * (i - units);
-                *reinterpret_cast<float4*>(y + e) = *reinterpret_cast<const float4*>(x + e);
+                a[k].x = x[ia];
+                if (i < units) b[k].x = x[P.adjacent ? ia + 1 : ia + half];
             }
-        } else {
-            if (i < units) {
-                const int ia = P.adjacent ? 2 * i : i, ib = P.adjacent ? 2 * i + 1 : half + i;
-                const float a = x[ia], b = x[ib];
-                const float2 c = cs[i];
-                y[ia] = a * c.x - b * c.y;
-                y[ib] = b * c.x + a * c.y;
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (kind[k] == 0) continue;
+            if (V == 4) {
+                if (kind[k] == 1) {
+                    // (cos, sin) of two pairs per load
+                    const float4* c = reinterpret_cast<const float4*>(cs + ci[k]);
+                    const float4 c0 = c[0], c1 = c[1], e = a[k], f = b[k];
+                    *reinterpret_cast<float4*>(y[k]) = make_float4(e.x * c0.x - f.x * c0.y, e.y * c0.z - f.y * c0.w,
+                                                                   e.z * c1.x - f.z * c1.y, e.w * c1.z - f.w * c1.w);
+                    *reinterpret_cast<float4*>(y[k] + half) = make_float4(f.x * c0.x + e.x * c0.y, f.y * c0.z + e.y * c0.w,
+                                                                          f.z * c1.x + e.z * c1.y, f.w * c1.z + e.w * c1.w);
+                } else {
+                    *reinterpret_cast<float4*>(y[k]) = a[k];
+                }
+            } else if (kind[k] == 1) {
+                const float2 c = cs[ci[k]];
+                y[k][0] = a[k].x * c.x - b[k].x * c.y;
+                y[k][P.adjacent ? 1 : half] = b[k].x * c.x + a[k].x * c.y;
             } else {
-                const int e = P.rot + (i - units);
-                y[e] = x[e];
+                y[k][0] = a[k].x;
             }
         }
     }
@@ -80,12 +113,18 @@ cudaError_t launch_rope(const RopeParams& P, int sms, cudaStream_t st) {
     // heads: 10 blocks)
     int split = 1;
     while (split * 4 < heads && (int64_t)P.ntok * split < sms) split *= 2;
-    const dim3 grid((unsigned)P.ntok, (unsigned)split);
     auto al16 = [](const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 4 == 0; };
     const bool vec = !P.adjacent && (P.rot / 2) % 4 == 0 && P.d % 4 == 0 && al16(P.q, P.ld_q) && al16(P.qo, P.ld_qo) &&
                      (P.n_k == 0 || (al16(P.k, P.ld_k) && al16(P.ko, P.ld_ko)));
-    if (vec) rope_kernel<4><<<grid, ROPE_THREADS, 0, st>>>(P);
-    else rope_kernel<1><<<grid, ROPE_THREADS, 0, st>>>(P);
+    // Many tokens: four per block, which has several loads per thread in flight
+    // and the table's latency once (one per block: 38 us for 8192 tokens of 12
+    // heads of 256, 5.3 TB/s).
+    const bool many = (int64_t)P.ntok >= 16 * (int64_t)sms;
+    const int tok = many ? ROPE_TOK : 1;
+    const dim3 grid((unsigned)((P.ntok + tok - 1) / tok), (unsigned)split);
+    const size_t smem = (size_t)(tok + 1) * (P.rot / 2) * 8;
+    auto kern = vec ? (many ? rope_kernel<4, ROPE_TOK> : rope_kernel<4, 1>) : (many ? rope_kernel<1, ROPE_TOK> : rope_kernel<1, 1>);
+    kern<<<grid, ROPE_THREADS, smem, st>>>(P);
     return cudaGetLastError();
 }
 
