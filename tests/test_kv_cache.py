@@ -677,3 +677,31 @@ def test_streams_and_graphs(lq):
         ref, bound = R.attn(c, table, start, np.arange(4), new[0], n_q, 0.1)
         check(out.cpu().numpy(), ref, bound, f"replay {i}")
     assert status(lq) == 0
+
+
+@pytest.mark.gpu
+def test_example_layer(lq):
+    """the example's prompts, decode graph, forks and compaction: finite outputs, equal samples equal, and the prompts' attention
+    over the appended cache against the 64-bit statement"""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import decode_layer as ex
+    y, outs, layer = ex.main(steps=3)
+    assert torch.isfinite(y).all()
+    for o in outs:
+        assert torch.isfinite(o).all()
+        assert torch.equal(o[2], o[3])
+    # one more decode step of row 0 (row 3 shares its prompt's pages): attention against the statement over the layer's own cache
+    P, rows = ex.PAGE, [0, 3]
+    start = layer.lens[rows].clone()
+    table = layer.table[rows].contiguous()
+    c = R.Cache(layer.n_pages, ex.N_KV, P, ex.D)
+    k, v, ks, vs = layer.cache.tensors
+    c.k, c.v = k.view(c.k.shape).cpu().numpy(), v.view(c.v.shape).cpu().numpy()
+    c.ks, c.vs = ks.cpu().numpy(), vs.cpu().numpy()
+    q = np.random.default_rng(3).standard_normal((2, ex.NQ)).astype(np.float32)
+    got = run_attn(lq, c, table.cpu().numpy(), (start - 1).tolist(), None, q, ex.N_Q, 0.0625, cache=layer.cache)
+    ref, bound = R.attn(c, table.cpu().numpy(), (start - 1).tolist(), np.arange(3), q, ex.N_Q, 0.0625)
+    check(got, ref, bound)
+    assert int((layer.ref > 0).sum()) == int((layer.table >= 0).sum()) - int((layer.ref - 1).clamp(min=0).sum())
