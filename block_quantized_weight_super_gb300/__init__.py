@@ -113,10 +113,22 @@ def _ptr(a):
     return a.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream():
+    """The calling thread's current stream of the current device, as an address.  torch.cuda.current_stream() makes a Stream object,
+    which takes 2.9 us of a small call's 8.9 us; the raw handle takes a few tenths.  Where torch has no such function, the object."""
+    global _raw_stream
+    import torch
+    if _raw_stream is None:
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(torch.cuda.current_device())
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
