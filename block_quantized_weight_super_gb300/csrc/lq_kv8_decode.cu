@@ -48,10 +48,12 @@ struct Dc {
     static constexpr int T = D == 64 ? 64 : 32;              // keys of a chunk
     static constexpr int TQ = T / 4;                         // keys of a quad pair
     static constexpr int NX = T / 16;                        // 16-key MMA tiles of a chunk
-    // warps: 2 to 4 per scheduler, as registers allow
-    static constexpr int NC = D == 256 ? 8 : NR == 1 ? 16 : 12;
+    // warps: 3 per scheduler, 2 where O takes the registers of 3 (32
+    // sequences of up to 8192 keys, D = 128: 12 warps 75 us, 14 84, 16 90,
+    // 10 85; with two row quads 106, 10 warps 121, 8 110)
+    static constexpr int NC = D == 256 ? 8 : 12;
     static constexpr int NT = NC * 32;
-    static constexpr int NSLOT = D == 256 ? 2 : 3;           // half-chunks of a warp's ring
+    static constexpr int NSLOT = D == 256 ? 2 : 3;           // half-chunks of a warp's ring (one more: 2 to 6 % slower)
     static constexpr int HB = T * D;                         // bytes of a half-chunk
     static constexpr int HBP = HB + 128;                     // with the padding between pages of V
     static constexpr bool QS = D == 256 && NR == 2;          // q fragments in shared memory (registers are full)
@@ -177,8 +179,12 @@ constexpr int DEC_MAX_SMS = 160;
 constexpr size_t COUNT_BYTES = 1024;
 __host__ __device__ constexpr int64_t part_floats(int d) { return MAX_RT * (int64_t)d + 2 * MAX_RT; }
 
+// a / b for a, b >= 0 (a 64-bit division takes hundreds of clocks).
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 // First worker of W whose share [U w / W, U (w + 1) / W) holds unit u.
-__device__ __forceinline__ int owner(int64_t u, int64_t U, int W) { return (int)(((u + 1) * W - 1) / U); }
+__device__ __forceinline__ int owner(int64_t u, int64_t U, int W) { return (int)quot((u + 1) * W - 1, U); }
 
 // A partial result: its tile's units [b0, b0 + nc) and rows.
 struct Stretch {
@@ -201,6 +207,7 @@ __global__ void __launch_bounds__(Dc<D, NR>::NT, 1) kv8_decode_kernel(const __gr
     __shared__ uint64_t full[NC][NSLOT];
     __shared__ Stretch parts[NC][2];                      // the partials that a warp left, and how many
     __shared__ int nparts[NC];
+    __shared__ uint32_t lasts;
     __shared__ int64_t first[NC + 1];                     // a warp's first unit; behind the last one's
     // what the end needs, out of the main loop's registers: the units in all,
     // warps in use per CTA, before this CTA, in this CTA
@@ -215,7 +222,6 @@ __global__ void __launch_bounds__(Dc<D, NR>::NT, 1) kv8_decode_kernel(const __gr
         mbar_init(&full[0][0] + tid, P.c.pshift == 4 ? T / 16 : P.c.pshift == 5 ? T / 32 : max(1, T >> P.c.pshift));
         fence_mbar_init();
     }
-    pdl_wait();
 
     // ---- the line: thread i sums the units of its sequences
     const int per = (P.s.nseq + NT - 1) / NT;
@@ -249,8 +255,11 @@ __global__ void __launch_bounds__(Dc<D, NR>::NT, 1) kv8_decode_kernel(const __gr
     {
         const int wpc = (int)min((int64_t)NC, (U + gridDim.x - 1) / gridDim.x);
         const int W = (int)min((int64_t)gridDim.x * wpc, U), w0 = blockIdx.x * wpc, act = min(wpc, W - w0);
-        if (act <= 0) return;                             // (the whole CTA)
-        if (tid <= act) first[tid] = U * (w0 + tid) / W;
+        if (act <= 0) {                                   // (the whole CTA)
+            pdl_wait();
+            return;
+        }
+        if (tid <= act) first[tid] = quot(U * (w0 + tid), W);
         if (tid == 0) {
             line.units = U;
             line.wpc = wpc;
@@ -274,10 +283,10 @@ __global__ void __launch_bounds__(Dc<D, NR>::NT, 1) kv8_decode_kernel(const __gr
             if (b + n > u0) break;
             b += n;
         }
-        const int64_t r = u0 - b, item = r / cc.d.nc;
-        cc.c = (int)(r % cc.d.nc);
-        cc.tile = (int)(item % cc.d.tiles);
-        cc.hk = (int)(item / cc.d.tiles);
+        const int64_t r = u0 - b, item = quot(r, cc.d.nc);
+        cc.c = (int)(r - item * cc.d.nc);
+        cc.hk = (int)quot(item, cc.d.tiles);
+        cc.tile = (int)(item - (int64_t)cc.hk * cc.d.tiles);
     }
     uint64_t* const bars = full[warp];
     const uint32_t wbase = smem_u32(smem) + warp * F::WB, qbase = wbase + NSLOT * F::HBP, mbase = qbase + F::QB;
@@ -658,135 +667,133 @@ __global__ void __launch_bounds__(Dc<D, NR>::NT, 1) kv8_decode_kernel(const __gr
     if (lane == 0) nparts[warp] = np;
     }
 
-    // ---- join the partials of the CTA's warps, then those of the CTAs: each
-    // warp the tiles whose first part in this CTA is its own
+    // ---- join the partials of the CTA's warps, then those of the CTAs: all
+    // warps, a row (or half of one) of a tile each.  Lane x looks at partial
+    // x & 1 of warp x / 2, which stands for its tile if it is the tile's first
+    // in this CTA.
+    pdl_wait();                                           // (the counters are clear)
     __syncthreads();
     const int64_t units = *(volatile int64_t*)&line.units;
     const int wpc = *(volatile int*)&line.wpc, w0 = *(volatile int*)&line.w0, act = *(volatile int*)&line.act;
     float* const part = reinterpret_cast<float*>(P.ws + COUNT_BYTES);
     constexpr int64_t PF = part_floats(D);
+    constexpr int HALF = D == 256 ? 2 : 1, V = D / HALF / 32, SL = RT * HALF;     // slices of a row; floats of a lane; slices
+    bool joins = false, crosses = false, inside = false, starts = false;
+    int e = 0, a = 0, ca = 0, cb = 0;                     // the tile's last warp in this CTA; its first worker, its CTAs
+    if ((lane >> 1) < act && (lane & 1) < nparts[lane >> 1]) {
+        const int w = lane >> 1;
+        const int64_t b0 = parts[w][lane & 1].b0, b1 = b0 + parts[w][lane & 1].nc;
+        starts = b0 >= first[w];
+        if (starts || w == 0) {
+            e = -1;
+#pragma unroll
+            for (int j = 0; j < NC; ++j) e += j < act && first[j] < b1;
+            inside = starts && b1 <= first[act];
+            const int W = (int)min((int64_t)gridDim.x * wpc, units);
+            a = starts ? w0 + w : owner(b0, units, W);
+            ca = a / wpc;
+            cb = inside ? ca : owner(b1 - 1, units, W) / wpc;
+            joins = e > w;                                // (a single one lies in the workspace already)
+            crosses = !inside;
+        }
+    }
 #pragma unroll 1
-    for (int i = 0; i < nparts[warp]; ++i) {
-        const Stretch s = parts[warp][i];
-        const bool starts = s.b0 >= first[warp];
-        if (!starts && warp > 0) continue;
-        const int64_t b1 = s.b0 + s.nc;
-        int e = warp;
-        while (e + 1 < act && first[e + 1] < b1) ++e;     // the last warp of the tile in this CTA
-        const bool inside = starts && b1 <= first[act];
-        // the tile's first worker, and the CTAs
-        const int W = (int)min((int64_t)gridDim.x * wpc, units);
-        const int a = starts ? w0 + warp : owner(s.b0, units, W), ca = a / wpc;
-        const int cb = inside ? ca : owner(b1 - 1, units, W) / wpc;
-        float* const own = part + (2 * (int64_t)(w0 + warp) + (starts ? 1 : 0)) * PF;
-#pragma unroll 1
-        for (int stage = 0; stage < 2; ++stage) {
-            const int n = stage ? cb - ca + 1 : e - warp + 1;
-            if (stage == 0 && n == 1) continue;           // already in the workspace
-            if (stage == 1) {
-                if (inside) break;
-                __threadfence();                          // the CTA's partial is out before it is counted
-                __syncwarp();
-                int k = 0;
-                if (lane == 0) k = atomicAdd(reinterpret_cast<int*>(P.ws) + ca, 1);
-                if (__shfl_sync(0xFFFFFFFFu, k, 0) != n - 1) break;
+    for (int stage = 0; stage < 2; ++stage) {
+        uint32_t todo = __ballot_sync(0xFFFFFFFFu, joins);
+        if (stage == 1) {
+            if (__ballot_sync(0xFFFFFFFFu, crosses) == 0) return;      // (the whole CTA)
+            __syncthreads();
+            if (warp == 0) {
+                __threadfence();                          // the CTA's partials are out before they are counted
+                const bool last = crosses && atomicAdd(reinterpret_cast<int*>(P.ws) + ca, 1) == cb - ca;
                 __threadfence();
+                const uint32_t b = __ballot_sync(0xFFFFFFFFu, last);
+                if (lane == 0) lasts = b;
             }
-            // lane x: where partial k0 + x lies, its maxima, its weights
-            constexpr int V4 = RT * D / 128;              // float4 of a partial per lane
-            float4 acc[V4];
-            float M[RT], l[RT];
+            __syncthreads();
+            todo = *(volatile uint32_t*)&lasts;
+        }
+#pragma unroll 1
+        for (int i = warp;; i += NC) {
+            uint32_t left = todo;
+            for (int j = i / SL; j > 0 && left; --j) left &= left - 1;
+            if (!left) break;
+            const int x = __ffs(left) - 1, w = x >> 1, r = i % SL / HALF, off = i % HALF * (D / HALF) + V * lane;
+            const int xe = __shfl_sync(0xFFFFFFFFu, e, x), xa = __shfl_sync(0xFFFFFFFFu, a, x), xca = __shfl_sync(0xFFFFFFFFu, ca, x);
+            const int n = stage ? __shfl_sync(0xFFFFFFFFu, cb, x) - xca + 1 : xe - w + 1;
+            const bool xstarts = __shfl_sync(0xFFFFFFFFu, (int)starts, x), xin = __shfl_sync(0xFFFFFFFFu, (int)inside, x);
+            const Stretch s = parts[w][x & 1];
+            if (r >= s.rows) continue;
+            float acc[V], M = -INFINITY, l = 0.f;
 #pragma unroll
-            for (int v = 0; v < V4; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                M[r] = -INFINITY;
-                l[r] = 0.f;
-            }
+            for (int v = 0; v < V; ++v) acc[v] = 0.f;
 #pragma unroll 1
             for (int k0 = 0; k0 < n; k0 += 32) {
+                // lane y: where partial k0 + y lies, its maximum, its weight
                 const int k = min(k0 + lane, n - 1);
-                const float* x;
+                const float* y;
                 if (stage) {
-                    const int y = max(a, (ca + k) * wpc);
-                    x = part + (2 * (int64_t)y + (y == a)) * PF;
+                    const int z = max(xa, (xca + k) * wpc);
+                    y = part + (2 * (int64_t)z + (z == xa)) * PF;
                 } else {
                     // (the last warp may have gone on with another tile: its ring was not free then)
-                    x = warp + k < e || b1 >= first[e + 1] ? reinterpret_cast<const float*>(smem + (warp + k) * F::WB)
-                                                           : part + 2 * (int64_t)(w0 + e) * PF;
+                    y = w + k < xe || s.b0 + s.nc >= first[xe + 1] ? reinterpret_cast<const float*>(smem + (w + k) * F::WB)
+                                                                   : part + 2 * (int64_t)(w0 + xe) * PF;
                 }
-                float c[RT];
+                const float mk = k0 + lane < n ? y[MAX_RT * D + 2 * r] : -INFINITY;
+                const float lk = k0 + lane < n ? y[MAX_RT * D + 2 * r + 1] : 0.f;
+                float mx = fmaxf(mk, M);
 #pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    const float mk = k0 + lane < n ? x[MAX_RT * D + 2 * r] : -INFINITY;
-                    const float lk = k0 + lane < n ? x[MAX_RT * D + 2 * r + 1] : 0.f;
-                    float mx = fmaxf(mk, M[r]);
+                for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+                const float f = M == mx ? 1.f : att_ex2(M - mx);
+                const float c = k0 + lane >= n ? 0.f : mk == mx ? 1.f : att_ex2(mk - mx);
+                M = mx;
+                l = fmaf(lk, c, l * f);
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-                    const float f = M[r] == mx ? 1.f : att_ex2(M[r] - mx);
-                    M[r] = mx;
-                    c[r] = k0 + lane >= n ? 0.f : mk == mx ? 1.f : att_ex2(mk - mx);
-                    l[r] = fmaf(lk, c[r], l[r] * f);
-#pragma unroll
-                    for (int v = 0; v < V4; ++v)
-                        if (128 * v / D <= r && r <= (128 * v + 127) / D && (D >= 128 || (lane >> 4) == (r & 1))) {
-                            acc[v].x *= f;
-                            acc[v].y *= f;
-                            acc[v].z *= f;
-                            acc[v].w *= f;
-                        }
-                }
+                for (int v = 0; v < V; ++v) acc[v] *= f;
+                y += r * D;
                 const int m = min(32, n - k0);
-                constexpr int KB = V4 >= 16 ? 1 : V4 >= 8 ? 2 : 4;          // partials at a time: their loads first
+                constexpr int KB = 8;                     // partials at a time: their loads first
 #pragma unroll 1
                 for (int kk = 0; kk < m; kk += KB) {
-                    float4 z[KB][V4];
+                    float z[KB][V];
 #pragma unroll
                     for (int b = 0; b < KB; ++b) {
-                        const float4* y = reinterpret_cast<const float4*>(
-                            __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(x), min(kk + b, m - 1))) + lane;
-#pragma unroll
-                        for (int v = 0; v < V4; ++v) z[b][v] = y[32 * v];
+                        const float* u = reinterpret_cast<const float*>(
+                                             __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(y), min(kk + b, m - 1))) + off;
+                        if constexpr (V == 4) {
+                            const float4 q = *reinterpret_cast<const float4*>(u);
+                            z[b][0] = q.x;
+                            z[b][1] = q.y;
+                            z[b][2] = q.z;
+                            z[b][3] = q.w;
+                        } else {
+                            const float2 q = *reinterpret_cast<const float2*>(u);
+                            z[b][0] = q.x;
+                            z[b][1] = q.y;
+                        }
                     }
 #pragma unroll
-                    for (int b = 0; b < KB; ++b)
+                    for (int b = 0; b < KB; ++b) {
+                        float ck = __shfl_sync(0xFFFFFFFFu, c, min(kk + b, m - 1));
+                        if (kk + b >= m) ck = 0.f;
 #pragma unroll
-                        for (int r = 0; r < RT; ++r) {
-                            float ck = __shfl_sync(0xFFFFFFFFu, c[r], min(kk + b, m - 1));
-                            if (kk + b >= m || r >= s.rows) ck = 0.f;
-#pragma unroll
-                            for (int v = 0; v < V4; ++v)
-                                if (128 * v / D <= r && r <= (128 * v + 127) / D && (D >= 128 || (lane >> 4) == (r & 1))) {
-                                    acc[v].x = fmaf(z[b][v].x, ck, acc[v].x);
-                                    acc[v].y = fmaf(z[b][v].y, ck, acc[v].y);
-                                    acc[v].z = fmaf(z[b][v].z, ck, acc[v].z);
-                                    acc[v].w = fmaf(z[b][v].w, ck, acc[v].w);
-                                }
-                        }
+                        for (int v = 0; v < V; ++v) acc[v] = fmaf(z[b][v], ck, acc[v]);
+                    }
                 }
             }
-            const bool final = stage == 1 || inside;
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+            const bool final = stage == 1 || xin;
+            float* const own = part + (2 * (int64_t)(w0 + w) + xstarts) * PF;
+            const int rt = s.r0 + r;
+            float* const y = final ? P.out + (int64_t)(s.row0 + rt / grp) * P.ld_out + (int64_t)(s.hk * grp + rt % grp) * D : own + r * D;
+            const float f = !final ? 1.f : l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], o);
-                if (r >= s.rows) continue;
-                const int rt = s.r0 + r;
-                float* y = final ? P.out + (int64_t)(s.row0 + rt / grp) * P.ld_out + (int64_t)(s.hk * grp + rt % grp) * D : own + r * D;
-                const float f = !final ? 1.f : l[r] == 0.f ? 0.f : 1.f / l[r];
-#pragma unroll
-                for (int v = 0; v < V4; ++v)
-                    if (128 * v / D <= r && r <= (128 * v + 127) / D && (D >= 128 || (lane >> 4) == (r & 1))) {
-                        const int d = (128 * v + 4 * lane) % D;
-                        y[d] = acc[v].x * f;
-                        y[d + 1] = acc[v].y * f;
-                        y[d + 2] = acc[v].z * f;
-                        y[d + 3] = acc[v].w * f;
-                    }
-                if (!final && lane == 0) {
-                    own[MAX_RT * D + 2 * r] = M[r];
-                    own[MAX_RT * D + 2 * r + 1] = l[r];
-                }
+            for (int v = 0; v < V; ++v) y[off + v] = acc[v] * f;
+            if (!final && lane == 0 && i % HALF == 0) {
+                own[MAX_RT * D + 2 * r] = M;
+                own[MAX_RT * D + 2 * r + 1] = l;
             }
         }
     }
@@ -832,7 +839,7 @@ constexpr int64_t PREFILL_MIN_ROWS = 64;
 }  // namespace
 
 size_t kv8_attn_workspace(int n_q, int n_kv, int d, int nseq, int ntok) {
-    const int nc = d == 256 ? Dc<256, 1>::NC : Dc<128, 1>::NC;           // the most warps of a CTA
+    const int nc = d == 256 ? Dc<256, 1>::NC : Dc<128, 1>::NC;
     return COUNT_BYTES + (size_t)DEC_MAX_SMS * nc * 2 * part_floats(d) * sizeof(float);
 }
 
