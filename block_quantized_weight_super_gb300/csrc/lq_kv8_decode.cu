@@ -151,6 +151,14 @@ __device__ __forceinline__ int64_t dec_units(const AttnParams& P, const DecSeq& 
     return (int64_t)P.c.n_kv * d.tiles * d.nc;
 }
 
+// Adds one to a counter; what this CTA wrote before its last barrier is out
+// before that, and what the others wrote before theirs is seen after it.
+__device__ __forceinline__ int count_in(int* c) {
+    int old;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(c) : "memory");
+    return old;
+}
+
 // A place in the line.
 struct Cur {
     DecSeq d;
@@ -704,9 +712,7 @@ __global__ void __launch_bounds__(Dc<D, NR>::NT, 1) kv8_decode_kernel(const __gr
             if (__ballot_sync(0xFFFFFFFFu, crosses) == 0) return;      // (the whole CTA)
             __syncthreads();
             if (warp == 0) {
-                __threadfence();                          // the CTA's partials are out before they are counted
-                const bool last = crosses && atomicAdd(reinterpret_cast<int*>(P.ws) + ca, 1) == cb - ca;
-                __threadfence();
+                const bool last = crosses && count_in(reinterpret_cast<int*>(P.ws) + ca) == cb - ca;
                 const uint32_t b = __ballot_sync(0xFFFFFFFFu, last);
                 if (lane == 0) lasts = b;
             }
@@ -742,25 +748,14 @@ __global__ void __launch_bounds__(Dc<D, NR>::NT, 1) kv8_decode_kernel(const __gr
                 }
                 const float mk = k0 + lane < n ? y[MAX_RT * D + 2 * r] : -INFINITY;
                 const float lk = k0 + lane < n ? y[MAX_RT * D + 2 * r + 1] : 0.f;
-                float mx = fmaxf(mk, M);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-                const float f = M == mx ? 1.f : att_ex2(M - mx);
-                const float c = k0 + lane >= n ? 0.f : mk == mx ? 1.f : att_ex2(mk - mx);
-                M = mx;
-                l = fmaf(lk, c, l * f);
-#pragma unroll
-                for (int v = 0; v < V; ++v) acc[v] *= f;
-                y += r * D;
                 const int m = min(32, n - k0);
                 constexpr int KB = 8;                     // partials at a time: their loads first
-#pragma unroll 1
-                for (int kk = 0; kk < m; kk += KB) {
-                    float z[KB][V];
+                float z[KB][V];
+                auto fetch = [&](int kk) {
 #pragma unroll
                     for (int b = 0; b < KB; ++b) {
                         const float* u = reinterpret_cast<const float*>(
-                                             __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(y), min(kk + b, m - 1))) + off;
+                                             __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(y), min(kk + b, m - 1))) + r * D + off;
                         if constexpr (V == 4) {
                             const float4 q = *reinterpret_cast<const float4*>(u);
                             z[b][0] = q.x;
@@ -773,6 +768,20 @@ __global__ void __launch_bounds__(Dc<D, NR>::NT, 1) kv8_decode_kernel(const __gr
                             z[b][1] = q.y;
                         }
                     }
+                };
+                fetch(0);
+                float mx = fmaxf(mk, M);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+                const float f = M == mx ? 1.f : att_ex2(M - mx);
+                const float c = k0 + lane >= n ? 0.f : mk == mx ? 1.f : att_ex2(mk - mx);
+                M = mx;
+                l = fmaf(lk, c, l * f);
+#pragma unroll
+                for (int v = 0; v < V; ++v) acc[v] *= f;
+#pragma unroll 1
+                for (int kk = 0; kk < m; kk += KB) {
+                    if (kk > 0) fetch(kk);
 #pragma unroll
                     for (int b = 0; b < KB; ++b) {
                         float ck = __shfl_sync(0xFFFFFFFFu, c, min(kk + b, m - 1));
