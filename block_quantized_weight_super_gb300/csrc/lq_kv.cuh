@@ -74,6 +74,27 @@ __device__ __forceinline__ uint32_t kv_round(float x, float s, float inv) {
     return __float_as_uint(t);
 }
 
+// The same for four values whose quotients are within 127.5, in a third of the
+// instructions: |d| < s / 2 shows that n is the nearest integer, which fails
+// next to a half-integer alone (about 2e-5 of all values).
+__device__ __forceinline__ void kv_round4(const float4& x, float s, float inv, uint32_t (&t)[4]) {
+    const float magic = 12582912.f;
+    const float2 a = make_float2(x.x, x.y), b = make_float2(x.z, x.w), i2 = make_float2(inv, inv);
+    const float2 ta = __ffma2_rn(a, i2, make_float2(magic, magic)), tb = __ffma2_rn(b, i2, make_float2(magic, magic));
+    const float2 na = __fadd2_rn(ta, make_float2(-magic, -magic)), nb = __fadd2_rn(tb, make_float2(-magic, -magic));
+    const float2 da = __ffma2_rn(na, make_float2(-s, -s), a), db = __ffma2_rn(nb, make_float2(-s, -s), b);
+    t[0] = __float_as_uint(ta.x);
+    t[1] = __float_as_uint(ta.y);
+    t[2] = __float_as_uint(tb.x);
+    t[3] = __float_as_uint(tb.y);
+    if (!(fmaxf(fmaxf(fabsf(da.x), fabsf(da.y)), fmaxf(fabsf(db.x), fabsf(db.y))) < 0.5f * s)) {
+        t[0] = kv_round(x.x, s, inv);
+        t[1] = kv_round(x.y, s, inv);
+        t[2] = kv_round(x.z, s, inv);
+        t[3] = kv_round(x.w, s, inv);
+    }
+}
+
 // Power of two that keeps the arithmetic of kv_round normal for tiny scales.
 __device__ __forceinline__ float kv_up(float s) { return s < 1e-30f ? 18446744073709551616.f : 1.f; }
 

@@ -124,7 +124,18 @@ __device__ __forceinline__ void append_full(const AppPage& p, bool isv, int pshi
     if (tid == 0) *p.scale = now;
     const bool good = kv_absbits(now) < 0x7F800000u && now > 0.f;
     const float up = kv_up(now), su = now * up, inv = 1.f / su;
-    auto code = [&](float x) -> uint32_t { return good ? kv_round(x * up, su, inv) : 0u; };
+    // the codes of four values, in the words' low bytes (a scale of a few
+    // subnormal steps may leave quotients above 127: clamped)
+    auto codes = [&](const float4& x, uint32_t (&t)[4]) {
+        if (good && up == 1.f) {
+            kv_round4(x, su, inv, t);
+        } else {
+            t[0] = good ? kv_round(x.x * up, su, inv) : 0u;
+            t[1] = good ? kv_round(x.y * up, su, inv) : 0u;
+            t[2] = good ? kv_round(x.z * up, su, inv) : 0u;
+            t[3] = good ? kv_round(x.w * up, su, inv) : 0u;
+        }
+    };
     for (int t0 = 0; t0 < n; t0 += TS) {
         if (n > TS) load(t0);                                // (one slab: still there)
 #pragma unroll
@@ -133,8 +144,11 @@ __device__ __forceinline__ void append_full(const AppPage& p, bool isv, int pshi
             if (t >= ts) continue;
             uint32_t w[4];                                   // codes of a token: 4 dims
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                w[k] = prmt(prmt(code(v[i][k].x), code(v[i][k].y), 0x0040u), prmt(code(v[i][k].z), code(v[i][k].w), 0x0040u), 0x5410u);
+            for (int k = 0; k < 4; ++k) {
+                uint32_t c[4];
+                codes(v[i][k], c);
+                w[k] = prmt(prmt(c[0], c[1], 0x0040u), prmt(c[2], c[3], 0x0040u), 0x5410u);
+            }
             if (!isv) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)

@@ -11,6 +11,8 @@
 #include "lq_internal.h"
 #include "lq_kv.cuh"
 
+#include <math_constants.h>
+
 namespace lq {
 namespace {
 
@@ -28,7 +30,9 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeParams P) 
     uint64_t* const turns = reinterpret_cast<uint64_t*>(cs + TOK * half);
     for (int i = threadIdx.x; i < half; i += ROPE_THREADS) {
         const double f = P.freq[i] * 0.15915494309189533577;
-        turns[i] = (uint64_t)((f - floor(f)) * 18446744073709551616.0);
+        const bool fine = fabs(f) < CUDART_INF;               // (else the pairs are copied)
+        if (!fine) record_status(P.status, STATUS_BADARG);
+        turns[i] = fine ? (uint64_t)fmin((f - floor(f)) * 18446744073709551616.0, 18446744073709549568.0) : 0;
     }
     __syncthreads();
     for (int u = threadIdx.x; u < half * nt; u += ROPE_THREADS) {

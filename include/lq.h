@@ -358,9 +358,11 @@ typedef struct {
  * 2i and 2i + 1.  Elements from rot_dim on are copied.  pos: [n_axes][ntok]
  * int32 (one axis for text; time, height, width ... for images and video);
  * axis: [rot_dim / 2] uint8, each < n_axes (NULL: axis 0); freq: [rot_dim / 2]
- * fp64, radians per position.  The angle is reduced in fp64, so positions of
- * any size keep fp32 accuracy.  q_out / k_out may equal q / k (with the same
- * ld); k may be NULL with n_k 0. */
+ * fp64, radians per position.  The angle is reduced in 64-bit fixed point, so
+ * positions of any size keep fp32 accuracy.  A pair whose axis or frequency is
+ * out of range (not finite) is copied and sets LQ_STATUS_BADARG.  q_out / k_out
+ * may equal q / k (with the same ld) and overlap them in no other way; k may
+ * be NULL with n_k 0. */
 enum { LQ_ROPE_HALF = 1, LQ_ROPE_ADJACENT = 2 };
 int lq_rope(const float* q, int n_q, int64_t ld_q, float* q_out, int64_t ld_qo, const float* k, int n_k,
             int64_t ld_k, float* k_out, int64_t ld_ko, int head_dim, int rot_dim, int pairing, const int32_t* pos,
@@ -398,7 +400,10 @@ int lq_kv8_append(const lq_kv8* cache, const int32_t* table, int max_pages, cons
  *   the softmax weights in two fp16 pieces each.  The result does not depend
  *   on the stream or on timing.  workspace:
  *   lq_kv8_attn_workspace_bytes(n_q, n_kv, head_dim, nseq, ntok) bytes, 256-byte
- *   aligned, scratch of this call only (invalid sizes give 0). */
+ *   aligned, scratch of this call only (invalid sizes give 0).  out overlaps
+ *   neither q nor the cache; it holds intermediate sums while the call runs.
+ *   The value scales of the pages that one row sees may differ by factors up
+ *   to 2^90 either way (beyond that the smaller ones count as that). */
 size_t lq_kv8_attn_workspace_bytes(int n_q, int n_kv, int head_dim, int nseq, int ntok);
 int lq_kv8_attn(const lq_kv8* cache, const int32_t* table, int max_pages, const int32_t* start, const int32_t* cu,
                 int nseq, const float* q, int n_q, int64_t ld_q, int ntok, float scale, float softcap, int window,

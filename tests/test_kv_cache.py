@@ -705,3 +705,23 @@ def test_example_layer(lq):
     ref, bound = R.attn(c, table.cpu().numpy(), (start - 1).tolist(), np.arange(3), q, ex.N_Q, 0.0625)
     check(got, ref, bound)
     assert int((layer.ref > 0).sum()) == int((layer.table >= 0).sum()) - int((layer.ref - 1).clamp(min=0).sum())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_rope_frequency_not_finite(lq, bad):
+    """a pair whose frequency is not finite is copied and reported; the others are rotated"""
+    import torch
+    x = torch.randn(3, 64, device="cuda")
+    freq = torch.ones(32, dtype=torch.float64, device="cuda")
+    freq[5] = bad
+    pos = torch.tensor([[1, 2, 3]], dtype=torch.int32, device="cuda")
+    out = torch.empty_like(x)
+    lq.lq_device_status()
+    lq.lq_rope(x, 1, 64, out, 64, None, 0, 0, None, 0, 64, 64, lq.LQ_ROPE_HALF, pos, 1, None, freq, 3)
+    rc, bits = lq.lq_device_status()
+    assert bits == 2
+    assert torch.equal(out[:, [5, 37]], x[:, [5, 37]])
+    c, s = torch.cos(pos[0].double()), torch.sin(pos[0].double())
+    want = x[:, 6].double() * c - x[:, 38].double() * s
+    assert (out[:, 6].double() - want).abs().max() < 4e-6
