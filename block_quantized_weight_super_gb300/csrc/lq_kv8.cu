@@ -35,6 +35,12 @@ __device__ __forceinline__ uint32_t app_max(uint32_t m, uint32_t* red) {
     for (int i = 0; i < NT / 32; ++i) m = max(m, red[i]);
     return m;
 }
+// max(m, |a|, |b|), NaN (as 0x7FFFFFFF) if one is.
+__device__ __forceinline__ float app_max3(float m, float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+    return d;
+}
 // The scale that a maximum asks for.
 __device__ __forceinline__ float app_scale(uint32_t m) {
     return m < 0x7F800000u ? __uint_as_float(m) * (1.f / 127.f) : __uint_as_float(0x7FC00000u);
@@ -111,16 +117,16 @@ __device__ __forceinline__ void append_full(const AppPage& p, bool isv, int pshi
                                                        : make_float4(0.f, 0.f, 0.f, 0.f);
         }
     };
-    uint32_t m = 0;
+    float m = 0.f;
     for (int t0 = 0; t0 < n; t0 += TS) {
         load(t0);
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                m = max(max(m, max(kv_absbits(v[i][k].x), kv_absbits(v[i][k].y))), max(kv_absbits(v[i][k].z), kv_absbits(v[i][k].w)));
+                m = app_max3(app_max3(m, v[i][k].x, v[i][k].y), v[i][k].z, v[i][k].w);
     }
-    const float now = app_scale(app_max<APP_FULL_THREADS>(m, red));
+    const float now = app_scale(app_max<APP_FULL_THREADS>(__float_as_uint(m), red));
     if (tid == 0) *p.scale = now;
     const bool good = kv_absbits(now) < 0x7F800000u && now > 0.f;
     const float up = kv_up(now), su = now * up, inv = 1.f / su;

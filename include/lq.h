@@ -402,8 +402,8 @@ int lq_kv8_append(const lq_kv8* cache, const int32_t* table, int max_pages, cons
  *   lq_kv8_attn_workspace_bytes(n_q, n_kv, head_dim, nseq, ntok) bytes, 256-byte
  *   aligned, scratch of this call only (invalid sizes give 0).  out overlaps
  *   neither q nor the cache; it holds intermediate sums while the call runs.
- *   The value scales of the pages that one row sees may differ by factors up
- *   to 2^90 either way (beyond that the smaller ones count as that). */
+ *   Value scales count relative to that of the first page a tile of rows
+ *   reads: below 2^-90 of it as 0, above 2^90 of it the row is NaN. */
 size_t lq_kv8_attn_workspace_bytes(int n_q, int n_kv, int head_dim, int nseq, int ntok);
 int lq_kv8_attn(const lq_kv8* cache, const int32_t* table, int max_pages, const int32_t* start, const int32_t* cu,
                 int nseq, const float* q, int n_q, int64_t ld_q, int ntok, float scale, float softcap, int window,
