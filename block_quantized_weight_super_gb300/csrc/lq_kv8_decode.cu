@@ -24,14 +24,19 @@
 // dealt to the warps of one CTA per SM in equal shares, whatever the lengths.
 // A warp keeps a running maximum, sum and O for its stretch of a tile.  A
 // stretch that is not a whole tile leaves a partial result in shared memory;
-// at the end the CTA's first warp of a tile joins those of its warps, and of the
+// at the end all warps of the CTA join them, a row of a tile each, and of the
 // CTAs that share a tile the last to finish joins theirs from the workspace (a
-// counter per CTA, which a first small kernel clears while this one is being
-// launched).
+// counter per CTA, which a first small kernel clears while this one begins).
 // Partials are joined in the order of the line whoever comes last, and the
 // shares depend on the lengths and the SM count only, so results are
-// reproducible.  (Joining in a second kernel cost 8 to 16 us.  The code here is
-// kept short: it runs once, from a cold instruction cache.)
+// reproducible.  (Joining in a second kernel cost 8 to 16 us; by one warp per
+// tile, 6 us of the 22 of one sequence of 4096 keys.  The code here is kept
+// short: it runs once, from a cold instruction cache.)
+//
+// Measured: 32 sequences of up to 8192 keys (417 MB) 77 us = 5.4 TB/s, the SMs'
+// issue slots half used; two of 131072 keys 88 us = 5.3 TB/s; without the joins
+// 6 us less.  One sequence of 4096 keys 16 us: launch, the search for the first
+// page, one chunk per warp and the joins, one memory latency after another.
 //
 // Loads.  Each warp streams its chunks through its own ring of half-chunks
 // (K, then V), always all but one of them in flight: bulk copies by its first
@@ -278,401 +283,401 @@ __global__ void __launch_bounds__(Dc<D, NR>::NT, 1) kv8_decode_kernel(const __gr
     if (lane == 0) nparts[warp] = 0;
     __syncthreads();
     if (warp < *(volatile int*)&line.act) {
-    const int nu = (int)(first[warp + 1] - first[warp]);
-    Cur cc;                                               // the unit at hand
-    {
-        const int64_t u0 = first[warp];
-        const int i = kv_find(NT, u0, [&](int x) { return tb[x]; });
-        int64_t b = tb[i];
-        int s = i * per;
-        for (;; ++s) {
-            cc.d = dec_seq<T, RT>(P, s);
-            const int64_t n = dec_units(P, cc.d);
-            if (b + n > u0) break;
-            b += n;
-        }
-        const int64_t r = u0 - b, item = quot(r, cc.d.nc);
-        cc.c = (int)(r - item * cc.d.nc);
-        cc.hk = (int)quot(item, cc.d.tiles);
-        cc.tile = (int)(item - (int64_t)cc.hk * cc.d.tiles);
-    }
-    uint64_t* const bars = full[warp];
-    const uint32_t wbase = smem_u32(smem) + warp * F::WB, qbase = wbase + NSLOT * F::HBP, mbase = qbase + F::QB;
-    const int pshift = P.c.pshift, Pg = 1 << pshift;
-
-    // ---- loading, ahead of the computation
-    Cur ci = cc;                                          // the unit to load
-    const int lpw = min(pshift, T == 64 ? 6 : 5), lnp = (T == 64 ? 6 : 5) - lpw;   // log2 of the keys a page gives a chunk, of its pages
-    // Lane x looks after page x & (pages - 1) of chunk wc + x / pages of this
-    // item: (page, head) in `win`, -1 if there is none.  It issues that page's
-    // copies itself, so issuing takes no shuffles.
-    int wc = ci.c, win = -1;
-    const int wl = lane >> lnp, wi = lane & ((1 << lnp) - 1);
-    auto window = [&]() {
-        wc = ci.c;
-        Cur k = ci;
-        k.c += wl;
-        const int pos = cur_chunk(k) * T + (wi << lpw);
-        const int pg = k.c < k.d.nc && pos < k.d.q.len ? att_page(P, k.d.q.s, pos) : -1;
-        win = pg < 0 ? -1 : pg * P.c.n_kv + ci.hk;
-    };
-    window();
-    const uint32_t pb = (uint32_t)D << lpw, blk = (uint32_t)D << pshift;      // bytes of a copy; of a page's head
-    const uint32_t vpad = lnp ? 128u >> lnp : 0u;
-    int hs = 0;                                           // slot of the half-chunk to load
-    auto issue = [&](int h) {                             // half-chunk h: K (even) or V (odd) of unit h / 2
-        if (h >= 2 * nu) return;
-        if (ci.c - wc == wl) {
-            uint64_t* bar = bars + hs;
-            const uint32_t dst = wbase + hs * F::HBP;
-            const int off = cur_chunk(ci) * T & (Pg - 1); // the chunk's place in its page (0 unless it is a part of it)
-            if ((h & 1) == 0) {
-                const uint32_t m = mbase + (h / 2 % F::NMETA) * 32 + 4 * wi;
-                if (win < 0) {
-                    st_sf(m, -1.f);                       // no such keys
-                    st_sf(m + 16, 0.f);
-                } else {
-                    cp4(m, P.c.ks + win);
-                    cp4(m + 16, P.c.vs + win);
-                    mbar_expect_tx(bar, pb);
-                    bulk_copy(dst + wi * pb, P.c.k + (int64_t)win * blk + off * D, pb, bar);
-                }
-                cp_arrive(bar);
-            } else if (win < 0) {
-                mbar_arrive(bar);
-            } else {
-                mbar_arrive_expect_tx(bar, pb);
-                if (lpw == pshift) bulk_copy(dst + wi * (pb + vpad), P.c.v + (int64_t)win * blk, pb, bar);
-                else tma_load_3d(dst, &vmap, off, 0, win, bar);
-            }
-        }
-        hs = hs + 1 == NSLOT ? 0 : hs + 1;
-        if ((h & 1) && h / 2 + 1 < nu) {
-            cur_next<T, RT>(P, ci);
-            if (ci.c == 0 || ci.c - wc >= 32 >> lnp) window();
-        }
-    };
-    for (int h = 0; h < NSLOT - 1; ++h) issue(h);
-
-    const int vw = min(Pg, T);                            // keys per row of V in shared memory
-    const uint32_t voff = (uint32_t)(TQ * t / vw) * ((uint32_t)vw * D + vpad) + (TQ * t) % vw + g * vw;
-    const uint32_t koff = (TQ * (g >> 1) + (g & 1)) * D + 16 * t, moff = (uint32_t)(TQ * (g >> 1) >> lpw) * 4;
-    float o[D / 16][NR][4];
-    uint32_t qf[F::QS ? 1 : D / 16][NR][2];
-    // of this thread's row t of each quad: maximum, sum, scale of the score,
-    // slope, position, and the keys it sees, [vlo, vhi) and [0, vpre)
-    float m[NR], l[NR], qs[NR], slope[NR];
-    int p[NR], vlo[NR], vhi[NR], vpre[NR];
-    int e0 = 0, np = 0;                                   // (np: partials left)
-    float is = 1.f;                                       // 2^-e0
-    bool fresh = true, from_start = false;
-
-    // Waits for half-chunk h; every lane is past the half before it then,
-    // whose slot is the next to fill.  On a timeout the halves in flight
-    // still land (bounded) before the warp leaves.
-    int cs = NSLOT - 1;                                   // slot of the half-chunk at hand, and its phase
-    uint32_t cph = 1;
-    auto arrived = [&](int h) -> bool {
-        cs = cs + 1 == NSLOT ? 0 : cs + 1;
-        cph ^= cs == 0;
-        if (__all_sync(0xFFFFFFFFu, att_wait(bars + cs, cph, P.timeout_ns))) return true;
-        record_status(P.status, STATUS_TIMEOUT);
-        for (int k = h; k < min(h + NSLOT - 1, 2 * nu); ++k)
-            mbar_wait_bounded(bars + k % NSLOT, (uint32_t)((k / NSLOT) & 1), drain_bound(P.timeout_ns));
-        return false;
-    };
-    for (int u = 0; u < nu; ++u) {
-        const AttSeq& q = cc.d.q;
-        if (fresh) {
-            // ---- a tile begins (or this warp's stretch of it): its rows
-            fresh = false;
-            from_start = cc.c == 0;
-            const int pe = att_page(P, q.s, cc.d.na > 0 ? 0 : min(cc.d.cb * T, q.len - 1));
-            const bool vec = ((reinterpret_cast<uintptr_t>(P.q) | (P.ld_q * 4)) & 15) == 0;
-            if (F::QS) __syncwarp();                      // every lane has read the last tile's fragments
-#pragma unroll
-            for (int z = 0; z < NR; ++z) {
-                // fragments: this thread makes the hi (g even) or lo piece of row g / 2
-                const int r = cc.tile * RT + 4 * z + (g >> 1);
-                const bool ok = r < q.n * grp;
-                const float* x = P.q + (int64_t)(q.row0 + (ok ? r / grp : 0)) * P.ld_q +
-                                 (int64_t)(cc.hk * grp + (ok ? r % grp : 0)) * D + 16 * t;
-                float mx = 0.f;
-                float v[D / 64][16];
-#pragma unroll
-                for (int a = 0; a < D / 64; ++a)
-#pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                        const float* y = x + 64 * a + e;
-                        if (ok) f = vec ? __ldg(reinterpret_cast<const float4*>(y)) : make_float4(__ldg(y), __ldg(y + 1), __ldg(y + 2), __ldg(y + 3));
-                        v[a][e] = f.x;
-                        v[a][e + 1] = f.y;
-                        v[a][e + 2] = f.z;
-                        v[a][e + 3] = f.w;
-                    }
-#pragma unroll
-                for (int a = 0; a < D / 64; ++a)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) mx = fmaxf(mx, fabsf(v[a][e]));
-                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-                // the row's power of two: |q| / 2^(es - 127) < 2^15
-                const int es = max(1, (int)((__float_as_uint(mx) >> 23) & 0xFFu) - 14);
-                const float inv = __uint_as_float((uint32_t)(254 - es) << 23);
-                qs[z] = __uint_as_float((uint32_t)__shfl_sync(0xFFFFFFFFu, es, 8 * t) << 23) * P.scale;   // of row t
-#pragma unroll
-                for (int a = 0; a < D / 64; ++a)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {         // MMA step 4 a + k: dims 64 a + 16 t + 4 k .. + 3
-                        uint32_t f[2], lo[2];
-                        att_split(v[a][4 * k] * inv, v[a][4 * k + 1] * inv, f[0], lo[0]);
-                        att_split(v[a][4 * k + 2] * inv, v[a][4 * k + 3] * inv, f[1], lo[1]);
-                        if (g & 1) {
-                            f[0] = lo[0];
-                            f[1] = lo[1];
-                        }
-                        if (F::QS) {
-                            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qbase + (((4 * a + k) * NR + z) * 32 + lane) * 8),
-                                         "r"(f[0]), "r"(f[1])
-                                         : "memory");     // (read back by this lane alone)
-                        } else {
-                            qf[F::QS ? 0 : 4 * a + k][z][0] = f[0];
-                            qf[F::QS ? 0 : 4 * a + k][z][1] = f[1];
-                        }
-                    }
-                // the softmax of row t
-                const int rt = cc.tile * RT + 4 * z + t;
-                const bool rok = rt < q.n * grp;
-                p[z] = (int)min(max(q.start + (rok ? rt / grp : 0), (int64_t)-1), (int64_t)INT32_MAX - 1);
-                vhi[z] = !rok ? INT32_MAX : p[z] < 0 ? 0 : min(p[z] + 1, q.len);
-                vlo[z] = rok && P.window ? max(p[z] - P.window + 1, 0) : 0;
-                vpre[z] = rok && p[z] >= 0 ? q.pre : 0;
-                slope[z] = EXTRA && P.slopes ? __ldg(P.slopes + cc.hk * grp + (rok ? rt % grp : 0)) : 0.f;
-                m[z] = -INFINITY;
-                l[z] = 0.f;
-            }
-            e0 = pe >= 0 ? att_e0(__ldg(P.c.vs + (int64_t)pe * P.c.n_kv + cc.hk)) : 0;
-            is = att_pow2(-e0);
-#pragma unroll
-            for (int n = 0; n < D / 16; ++n)
-#pragma unroll
-                for (int z = 0; z < NR; ++z)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[n][z][e] = 0.f;
-        }
-
-        // ---- S^T = K Q^T
-        const int hK = 2 * u;
-        if (!arrived(hK)) break;
-        issue(hK + NSLOT - 1);
-        const uint32_t mt = mbase + (u % F::NMETA) * 32 + moff;
-        const float ks = ld_sf(mt), vs = ld_sf(mt + 16);
-        const bool held = !(ks < 0.f);
-        float s[NX][NR][4];
+        const int nu = (int)(first[warp + 1] - first[warp]);
+        Cur cc;                                               // the unit at hand
         {
-            const uint32_t kb = wbase + cs * F::HBP + koff;
-#pragma unroll
-            for (int a = 0; a < D / 64; ++a) {
-                uint32_t qa[4][NR][2];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int z = 0; z < NR; ++z) {
-                        if (F::QS) {
-                            const uint2 f = ld_s64(qbase + (((4 * a + k) * NR + z) * 32 + lane) * 8);
-                            qa[k][z][0] = f.x;
-                            qa[k][z][1] = f.y;
-                        } else {
-                            qa[k][z][0] = qf[F::QS ? 0 : 4 * a + k][z][0];
-                            qa[k][z][1] = qf[F::QS ? 0 : 4 * a + k][z][1];
-                        }
+            const int64_t u0 = first[warp];
+            const int i = kv_find(NT, u0, [&](int x) { return tb[x]; });
+            int64_t b = tb[i];
+            int s = i * per;
+            for (;; ++s) {
+                cc.d = dec_seq<T, RT>(P, s);
+                const int64_t n = dec_units(P, cc.d);
+                if (b + n > u0) break;
+                b += n;
+            }
+            const int64_t r = u0 - b, item = quot(r, cc.d.nc);
+            cc.c = (int)(r - item * cc.d.nc);
+            cc.hk = (int)quot(item, cc.d.tiles);
+            cc.tile = (int)(item - (int64_t)cc.hk * cc.d.tiles);
+        }
+        uint64_t* const bars = full[warp];
+        const uint32_t wbase = smem_u32(smem) + warp * F::WB, qbase = wbase + NSLOT * F::HBP, mbase = qbase + F::QB;
+        const int pshift = P.c.pshift, Pg = 1 << pshift;
+
+        // ---- loading, ahead of the computation
+        Cur ci = cc;                                          // the unit to load
+        const int lpw = min(pshift, T == 64 ? 6 : 5), lnp = (T == 64 ? 6 : 5) - lpw;   // log2 of the keys a page gives a chunk, of its pages
+        // Lane x looks after page x & (pages - 1) of chunk wc + x / pages of this
+        // item: (page, head) in `win`, -1 if there is none.  It issues that page's
+        // copies itself, so issuing takes no shuffles.
+        int wc = ci.c, win = -1;
+        const int wl = lane >> lnp, wi = lane & ((1 << lnp) - 1);
+        auto window = [&]() {
+            wc = ci.c;
+            Cur k = ci;
+            k.c += wl;
+            const int pos = cur_chunk(k) * T + (wi << lpw);
+            const int pg = k.c < k.d.nc && pos < k.d.q.len ? att_page(P, k.d.q.s, pos) : -1;
+            win = pg < 0 ? -1 : pg * P.c.n_kv + ci.hk;
+        };
+        window();
+        const uint32_t pb = (uint32_t)D << lpw, blk = (uint32_t)D << pshift;      // bytes of a copy; of a page's head
+        const uint32_t vpad = lnp ? 128u >> lnp : 0u;
+        int hs = 0;                                           // slot of the half-chunk to load
+        auto issue = [&](int h) {                             // half-chunk h: K (even) or V (odd) of unit h / 2
+            if (h >= 2 * nu) return;
+            if (ci.c - wc == wl) {
+                uint64_t* bar = bars + hs;
+                const uint32_t dst = wbase + hs * F::HBP;
+                const int off = cur_chunk(ci) * T & (Pg - 1); // the chunk's place in its page (0 unless it is a part of it)
+                if ((h & 1) == 0) {
+                    const uint32_t m = mbase + (h / 2 % F::NMETA) * 32 + 4 * wi;
+                    if (win < 0) {
+                        st_sf(m, -1.f);                       // no such keys
+                        st_sf(m + 16, 0.f);
+                    } else {
+                        cp4(m, P.c.ks + win);
+                        cp4(m + 16, P.c.vs + win);
+                        mbar_expect_tx(bar, pb);
+                        bulk_copy(dst + wi * pb, P.c.k + (int64_t)win * blk + off * D, pb, bar);
                     }
-#pragma unroll
-                for (int x = 0; x < NX; ++x) {
-                    // keys of tile rows g and g + 8
-                    const uint4 k0 = ld_s128(kb + 4 * x * D + 64 * a), k1 = ld_s128(kb + (4 * x + 2) * D + 64 * a);
-                    const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t f[4];
-                        att_codes(w0[k], f[0], f[2]);
-                        att_codes(w1[k], f[1], f[3]);
-#pragma unroll
-                        for (int z = 0; z < NR; ++z) {
-                            if (a == 0 && k == 0) mma16816_first(s[x][z], f, qa[k][z][0], qa[k][z][1]);
-                            else mma16816(s[x][z], f, qa[k][z][0], qa[k][z][1]);
-                        }
-                    }
+                    cp_arrive(bar);
+                } else if (win < 0) {
+                    mbar_arrive(bar);
+                } else {
+                    mbar_arrive_expect_tx(bar, pb);
+                    if (lpw == pshift) bulk_copy(dst + wi * (pb + vpad), P.c.v + (int64_t)win * blk, pb, bar);
+                    else tma_load_3d(dst, &vmap, off, 0, win, bar);
                 }
             }
-        }
+            hs = hs + 1 == NSLOT ? 0 : hs + 1;
+            if ((h & 1) && h / 2 + 1 < nu) {
+                cur_next<T, RT>(P, ci);
+                if (ci.c == 0 || ci.c - wc >= 32 >> lnp) window();
+            }
+        };
+        for (int h = 0; h < NSLOT - 1; ++h) issue(h);
 
-        // ---- weights
-        const int j0 = cur_chunk(cc) * T, jt = j0 + TQ * (g >> 1) + (g & 1);
-        bool whole = held;
+        const int vw = min(Pg, T);                            // keys per row of V in shared memory
+        const uint32_t voff = (uint32_t)(TQ * t / vw) * ((uint32_t)vw * D + vpad) + (TQ * t) % vw + g * vw;
+        const uint32_t koff = (TQ * (g >> 1) + (g & 1)) * D + 16 * t, moff = (uint32_t)(TQ * (g >> 1) >> lpw) * 4;
+        float o[D / 16][NR][4];
+        uint32_t qf[F::QS ? 1 : D / 16][NR][2];
+        // of this thread's row t of each quad: maximum, sum, scale of the score,
+        // slope, position, and the keys it sees, [vlo, vhi) and [0, vpre)
+        float m[NR], l[NR], qs[NR], slope[NR];
+        int p[NR], vlo[NR], vhi[NR], vpre[NR];
+        int e0 = 0, np = 0;                                   // (np: partials left)
+        float is = 1.f;                                       // 2^-e0
+        bool fresh = true, from_start = false;
+
+        // Waits for half-chunk h; every lane is past the half before it then,
+        // whose slot is the next to fill.  On a timeout the halves in flight
+        // still land (bounded) before the warp leaves.
+        int cs = NSLOT - 1;                                   // slot of the half-chunk at hand, and its phase
+        uint32_t cph = 1;
+        auto arrived = [&](int h) -> bool {
+            cs = cs + 1 == NSLOT ? 0 : cs + 1;
+            cph ^= cs == 0;
+            if (__all_sync(0xFFFFFFFFu, att_wait(bars + cs, cph, P.timeout_ns))) return true;
+            record_status(P.status, STATUS_TIMEOUT);
+            for (int k = h; k < min(h + NSLOT - 1, 2 * nu); ++k)
+                mbar_wait_bounded(bars + k % NSLOT, (uint32_t)((k / NSLOT) & 1), drain_bound(P.timeout_ns));
+            return false;
+        };
+        for (int u = 0; u < nu; ++u) {
+            const AttSeq& q = cc.d.q;
+            if (fresh) {
+                // ---- a tile begins (or this warp's stretch of it): its rows
+                fresh = false;
+                from_start = cc.c == 0;
+                const int pe = att_page(P, q.s, cc.d.na > 0 ? 0 : min(cc.d.cb * T, q.len - 1));
+                const bool vec = ((reinterpret_cast<uintptr_t>(P.q) | (P.ld_q * 4)) & 15) == 0;
+                if (F::QS) __syncwarp();                      // every lane has read the last tile's fragments
 #pragma unroll
-        for (int z = 0; z < NR; ++z) whole = whole && (j0 + T <= vpre[z] || (j0 >= vlo[z] && j0 + T <= vhi[z]));
-        const bool all_whole = __all_sync(0xFFFFFFFFu, whole);
-        bool vzero;
-        const float rel = att_rel(vs * is, vzero), lv = att_lg2(rel);
-        uint32_t wb[NX][NR][2];
+                for (int z = 0; z < NR; ++z) {
+                    // fragments: this thread makes the hi (g even) or lo piece of row g / 2
+                    const int r = cc.tile * RT + 4 * z + (g >> 1);
+                    const bool ok = r < q.n * grp;
+                    const float* x = P.q + (int64_t)(q.row0 + (ok ? r / grp : 0)) * P.ld_q +
+                                     (int64_t)(cc.hk * grp + (ok ? r % grp : 0)) * D + 16 * t;
+                    float mx = 0.f;
+                    float v[D / 64][16];
 #pragma unroll
-        for (int z = 0; z < NR; ++z) {
-            const float f = qs[z] * ks * (EXTRA ? 1.f : ATT_LOG2E);
-            float v[NX][2], mx = -INFINITY;
+                    for (int a = 0; a < D / 64; ++a)
 #pragma unroll
-            for (int x = 0; x < NX; ++x)
+                        for (int e = 0; e < 16; e += 4) {
+                            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                            const float* y = x + 64 * a + e;
+                            if (ok) f = vec ? __ldg(reinterpret_cast<const float4*>(y)) : make_float4(__ldg(y), __ldg(y + 1), __ldg(y + 2), __ldg(y + 3));
+                            v[a][e] = f.x;
+                            v[a][e + 1] = f.y;
+                            v[a][e + 2] = f.z;
+                            v[a][e + 3] = f.w;
+                        }
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float y = s[x][z][2 * e] + s[x][z][2 * e + 1];
-                    const int j = jt + 4 * x + 2 * e;
-                    if (EXTRA) {
-                        y *= f;
-                        if (P.softcap > 0.f) y = P.softcap * att_tanh(__fdividef(y, P.softcap));
-                        y -= slope[z] * fabsf((float)(p[z] - j));
-                        y = fmaf(y, ATT_LOG2E, lv);
-                    } else {
-                        y = fmaf(y, f, lv);
-                    }
-                    if (!all_whole) {
-                        const bool see = j < vpre[z] || (j >= vlo[z] && j < vhi[z]);
-                        if (see && !held && vhi[z] != INT32_MAX) record_status(P.status, STATUS_BADARG);
-                        if (!see || !held) y = -INFINITY;
-                    }
-                    v[x][e] = y;
-                    mx = fmaxf(mx, y);
+                    for (int a = 0; a < D / 64; ++a)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) mx = fmaxf(mx, fabsf(v[a][e]));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+                    // the row's power of two: |q| / 2^(es - 127) < 2^15
+                    const int es = max(1, (int)((__float_as_uint(mx) >> 23) & 0xFFu) - 14);
+                    const float inv = __uint_as_float((uint32_t)(254 - es) << 23);
+                    qs[z] = __uint_as_float((uint32_t)__shfl_sync(0xFFFFFFFFu, es, 8 * t) << 23) * P.scale;   // of row t
+#pragma unroll
+                    for (int a = 0; a < D / 64; ++a)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {         // MMA step 4 a + k: dims 64 a + 16 t + 4 k .. + 3
+                            uint32_t f[2], lo[2];
+                            att_split(v[a][4 * k] * inv, v[a][4 * k + 1] * inv, f[0], lo[0]);
+                            att_split(v[a][4 * k + 2] * inv, v[a][4 * k + 3] * inv, f[1], lo[1]);
+                            if (g & 1) {
+                                f[0] = lo[0];
+                                f[1] = lo[1];
+                            }
+                            if (F::QS) {
+                                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qbase + (((4 * a + k) * NR + z) * 32 + lane) * 8),
+                                             "r"(f[0]), "r"(f[1])
+                                             : "memory");     // (read back by this lane alone)
+                            } else {
+                                qf[F::QS ? 0 : 4 * a + k][z][0] = f[0];
+                                qf[F::QS ? 0 : 4 * a + k][z][1] = f[1];
+                            }
+                        }
+                    // the softmax of row t
+                    const int rt = cc.tile * RT + 4 * z + t;
+                    const bool rok = rt < q.n * grp;
+                    p[z] = (int)min(max(q.start + (rok ? rt / grp : 0), (int64_t)-1), (int64_t)INT32_MAX - 1);
+                    vhi[z] = !rok ? INT32_MAX : p[z] < 0 ? 0 : min(p[z] + 1, q.len);
+                    vlo[z] = rok && P.window ? max(p[z] - P.window + 1, 0) : 0;
+                    vpre[z] = rok && p[z] >= 0 ? q.pre : 0;
+                    slope[z] = EXTRA && P.slopes ? __ldg(P.slopes + cc.hk * grp + (rok ? rt % grp : 0)) : 0.f;
+                    m[z] = -INFINITY;
+                    l[z] = 0.f;
                 }
-            // no key of this thread seen: its page's scale, which may be NaN,
-            // does not count (a seen key of a NaN page still makes its weight NaN)
-            const float il = mx == -INFINITY ? 0.f : att_rcp(rel);
-            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
-            if (__any_sync(0xFFFFFFFFu, mx > m[z])) {
-                const float mn = fmaxf(m[z], mx), r = m[z] == mn ? 1.f : att_ex2(m[z] - mn);
-                m[z] = mn;
-                l[z] *= r;
+                e0 = pe >= 0 ? att_e0(__ldg(P.c.vs + (int64_t)pe * P.c.n_kv + cc.hk)) : 0;
+                is = att_pow2(-e0);
 #pragma unroll
                 for (int n = 0; n < D / 16; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[n][z][e] *= r;
+                    for (int z = 0; z < NR; ++z)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[n][z][e] = 0.f;
             }
-            const float ref = m[z] == -INFINITY ? 0.f : m[z] - ATT_SHIFT;
-            float sum = 0.f;
+
+            // ---- S^T = K Q^T
+            const int hK = 2 * u;
+            if (!arrived(hK)) break;
+            issue(hK + NSLOT - 1);
+            const uint32_t mt = mbase + (u % F::NMETA) * 32 + moff;
+            const float ks = ld_sf(mt), vs = ld_sf(mt + 16);
+            const bool held = !(ks < 0.f);
+            float s[NX][NR][4];
+            {
+                const uint32_t kb = wbase + cs * F::HBP + koff;
 #pragma unroll
-            for (int x = 0; x < NX; ++x)
+                for (int a = 0; a < D / 64; ++a) {
+                    uint32_t qa[4][NR][2];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float y = att_ex2(v[x][e] - ref);
-                    sum += y;
-                    wb[x][z][e] = split1(y);
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int z = 0; z < NR; ++z) {
+                            if (F::QS) {
+                                const uint2 f = ld_s64(qbase + (((4 * a + k) * NR + z) * 32 + lane) * 8);
+                                qa[k][z][0] = f.x;
+                                qa[k][z][1] = f.y;
+                            } else {
+                                qa[k][z][0] = qf[F::QS ? 0 : 4 * a + k][z][0];
+                                qa[k][z][1] = qf[F::QS ? 0 : 4 * a + k][z][1];
+                            }
+                        }
+#pragma unroll
+                    for (int x = 0; x < NX; ++x) {
+                        // keys of tile rows g and g + 8
+                        const uint4 k0 = ld_s128(kb + 4 * x * D + 64 * a), k1 = ld_s128(kb + (4 * x + 2) * D + 64 * a);
+                        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t f[4];
+                            att_codes(w0[k], f[0], f[2]);
+                            att_codes(w1[k], f[1], f[3]);
+#pragma unroll
+                            for (int z = 0; z < NR; ++z) {
+                                if (a == 0 && k == 0) mma16816_first(s[x][z], f, qa[k][z][0], qa[k][z][1]);
+                                else mma16816(s[x][z], f, qa[k][z][0], qa[k][z][1]);
+                            }
+                        }
+                    }
                 }
-            l[z] = fmaf(sum, il, l[z]);
-        }
-        if (__any_sync(0xFFFFFFFFu, vzero)) {
-            const uint32_t vmask = vzero ? 0u : 0xFFFFFFFFu;
+            }
+
+            // ---- weights
+            const int j0 = cur_chunk(cc) * T, jt = j0 + TQ * (g >> 1) + (g & 1);
+            bool whole = held;
+#pragma unroll
+            for (int z = 0; z < NR; ++z) whole = whole && (j0 + T <= vpre[z] || (j0 >= vlo[z] && j0 + T <= vhi[z]));
+            const bool all_whole = __all_sync(0xFFFFFFFFu, whole);
+            bool vzero;
+            const float rel = att_rel(vs * is, vzero), lv = att_lg2(rel);
+            uint32_t wb[NX][NR][2];
+#pragma unroll
+            for (int z = 0; z < NR; ++z) {
+                const float f = qs[z] * ks * (EXTRA ? 1.f : ATT_LOG2E);
+                float v[NX][2], mx = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < NX; ++x)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float y = s[x][z][2 * e] + s[x][z][2 * e + 1];
+                        const int j = jt + 4 * x + 2 * e;
+                        if (EXTRA) {
+                            y *= f;
+                            if (P.softcap > 0.f) y = P.softcap * att_tanh(__fdividef(y, P.softcap));
+                            y -= slope[z] * fabsf((float)(p[z] - j));
+                            y = fmaf(y, ATT_LOG2E, lv);
+                        } else {
+                            y = fmaf(y, f, lv);
+                        }
+                        if (!all_whole) {
+                            const bool see = j < vpre[z] || (j >= vlo[z] && j < vhi[z]);
+                            if (see && !held && vhi[z] != INT32_MAX) record_status(P.status, STATUS_BADARG);
+                            if (!see || !held) y = -INFINITY;
+                        }
+                        v[x][e] = y;
+                        mx = fmaxf(mx, y);
+                    }
+                // no key of this thread seen: its page's scale, which may be NaN,
+                // does not count (a seen key of a NaN page still makes its weight NaN)
+                const float il = mx == -INFINITY ? 0.f : att_rcp(rel);
+                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+                if (__any_sync(0xFFFFFFFFu, mx > m[z])) {
+                    const float mn = fmaxf(m[z], mx), r = m[z] == mn ? 1.f : att_ex2(m[z] - mn);
+                    m[z] = mn;
+                    l[z] *= r;
+#pragma unroll
+                    for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[n][z][e] *= r;
+                }
+                const float ref = m[z] == -INFINITY ? 0.f : m[z] - ATT_SHIFT;
+                float sum = 0.f;
+#pragma unroll
+                for (int x = 0; x < NX; ++x)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float y = att_ex2(v[x][e] - ref);
+                        sum += y;
+                        wb[x][z][e] = split1(y);
+                    }
+                l[z] = fmaf(sum, il, l[z]);
+            }
+            if (__any_sync(0xFFFFFFFFu, vzero)) {
+                const uint32_t vmask = vzero ? 0u : 0xFFFFFFFFu;
+#pragma unroll
+                for (int x = 0; x < NX; ++x)
+#pragma unroll
+                    for (int z = 0; z < NR; ++z) {
+                        wb[x][z][0] &= vmask;
+                        wb[x][z][1] &= vmask;
+                    }
+            }
 #pragma unroll
             for (int x = 0; x < NX; ++x)
 #pragma unroll
                 for (int z = 0; z < NR; ++z) {
-                    wb[x][z][0] &= vmask;
-                    wb[x][z][1] &= vmask;
+                    wb[x][z][0] = transpose8(wb[x][z][0]);
+                    wb[x][z][1] = transpose8(wb[x][z][1]);
                 }
-        }
-#pragma unroll
-        for (int x = 0; x < NX; ++x)
-#pragma unroll
-            for (int z = 0; z < NR; ++z) {
-                wb[x][z][0] = transpose8(wb[x][z][0]);
-                wb[x][z][1] = transpose8(wb[x][z][1]);
-            }
 
-        // ---- O^T += V^T W^T
-        const int hV = hK + 1;
-        if (!arrived(hV)) break;
-        issue(hV + NSLOT - 1);
-        {
-            const uint32_t vb = wbase + cs * F::HBP + voff;
-#pragma unroll
-            for (int n = 0; n < D / 16; ++n) {
-                uint32_t w0[4], w1[4];                    // dims 16 n + g and + 8
-                if (T == 64) {
-                    const uint4 a = ld_s128(vb + 16 * n * vw), b = ld_s128(vb + (16 * n + 8) * vw);
-                    w0[0] = a.x;
-                    w0[1] = a.y;
-                    w0[2] = a.z;
-                    w0[3] = a.w;
-                    w1[0] = b.x;
-                    w1[1] = b.y;
-                    w1[2] = b.z;
-                    w1[3] = b.w;
-                } else {
-                    const uint2 a = ld_s64(vb + 16 * n * vw), b = ld_s64(vb + (16 * n + 8) * vw);
-                    w0[0] = a.x;
-                    w0[1] = a.y;
-                    w1[0] = b.x;
-                    w1[1] = b.y;
-                }
-#pragma unroll
-                for (int x = 0; x < NX; ++x) {
-                    uint32_t f[4];
-                    att_codes(w0[x], f[0], f[2]);
-                    att_codes(w1[x], f[1], f[3]);
-#pragma unroll
-                    for (int z = 0; z < NR; ++z) mma16816(o[n][z], f, wb[x][z][0], wb[x][z][1]);
-                }
-            }
-        }
-
-        // ---- the tile, or this warp's stretch of it, ends
-        const bool tile_end = cc.c == cc.d.nc - 1;
-        if (tile_end || u == nu - 1) {
-            const float up = att_pow2(e0);
-            const bool whole_tile = tile_end && from_start;
-            // a partial goes to this warp's ring if that is done with, unless
-            // the CTA has no other of the tile
-            const int64_t b0 = first[warp] + u - cc.c, b1 = b0 + cc.d.nc;
-            const int act = *(volatile int*)&line.act, w0 = *(volatile int*)&line.w0;
-            const bool alone = (warp == 0 || b0 >= first[warp]) && (warp == act - 1 || b1 <= first[warp + 1]);
-            float* const mine = !alone && u == nu - 1
-                                    ? reinterpret_cast<float*>(smem + warp * F::WB)
-                                    : reinterpret_cast<float*>(P.ws + COUNT_BYTES) + (2 * (int64_t)(w0 + warp) + (from_start ? 1 : 0)) * part_floats(D);
-#pragma unroll
-            for (int z = 0; z < NR; ++z) {
-                float sum = l[z];
-                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 4);
-                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
-                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
-                const int rt = cc.tile * RT + 4 * z + t;
-                if (rt >= q.n * grp) continue;
-                float* y;
-                float r;
-                if (whole_tile) {
-                    y = P.out + (int64_t)(q.row0 + rt / grp) * P.ld_out + (int64_t)(cc.hk * grp + rt % grp) * D;
-                    r = sum == 0.f ? 0.f : up / sum;
-                } else {
-                    y = mine;
-                    if (g == 0) *reinterpret_cast<float2*>(y + MAX_RT * D + 2 * (4 * z + t)) = make_float2(m[z], sum);
-                    y += (4 * z + t) * D;
-                    r = up;
-                }
+            // ---- O^T += V^T W^T
+            const int hV = hK + 1;
+            if (!arrived(hV)) break;
+            issue(hV + NSLOT - 1);
+            {
+                const uint32_t vb = wbase + cs * F::HBP + voff;
 #pragma unroll
                 for (int n = 0; n < D / 16; ++n) {
-                    y[16 * n + g] = (o[n][z][0] + o[n][z][1]) * r;
-                    y[16 * n + 8 + g] = (o[n][z][2] + o[n][z][3]) * r;
+                    uint32_t w0[4], w1[4];                    // dims 16 n + g and + 8
+                    if (T == 64) {
+                        const uint4 a = ld_s128(vb + 16 * n * vw), b = ld_s128(vb + (16 * n + 8) * vw);
+                        w0[0] = a.x;
+                        w0[1] = a.y;
+                        w0[2] = a.z;
+                        w0[3] = a.w;
+                        w1[0] = b.x;
+                        w1[1] = b.y;
+                        w1[2] = b.z;
+                        w1[3] = b.w;
+                    } else {
+                        const uint2 a = ld_s64(vb + 16 * n * vw), b = ld_s64(vb + (16 * n + 8) * vw);
+                        w0[0] = a.x;
+                        w0[1] = a.y;
+                        w1[0] = b.x;
+                        w1[1] = b.y;
+                    }
+#pragma unroll
+                    for (int x = 0; x < NX; ++x) {
+                        uint32_t f[4];
+                        att_codes(w0[x], f[0], f[2]);
+                        att_codes(w1[x], f[1], f[3]);
+#pragma unroll
+                        for (int z = 0; z < NR; ++z) mma16816(o[n][z], f, wb[x][z][0], wb[x][z][1]);
+                    }
                 }
             }
-            fresh = true;
-            if (!whole_tile) {
-                if (lane == 0) parts[warp][np] = Stretch{b0, cc.d.nc, q.row0, cc.hk, cc.tile * RT, min(RT, q.n * grp - cc.tile * RT)};
-                ++np;
-            }
-        }
-        if (u < nu - 1) cur_next<T, RT>(P, cc);
-    }
 
-    if (lane == 0) nparts[warp] = np;
+            // ---- the tile, or this warp's stretch of it, ends
+            const bool tile_end = cc.c == cc.d.nc - 1;
+            if (tile_end || u == nu - 1) {
+                const float up = att_pow2(e0);
+                const bool whole_tile = tile_end && from_start;
+                // a partial goes to this warp's ring if that is done with, unless
+                // the CTA has no other of the tile
+                const int64_t b0 = first[warp] + u - cc.c, b1 = b0 + cc.d.nc;
+                const int act = *(volatile int*)&line.act, w0 = *(volatile int*)&line.w0;
+                const bool alone = (warp == 0 || b0 >= first[warp]) && (warp == act - 1 || b1 <= first[warp + 1]);
+                float* const mine = !alone && u == nu - 1
+                                        ? reinterpret_cast<float*>(smem + warp * F::WB)
+                                        : reinterpret_cast<float*>(P.ws + COUNT_BYTES) + (2 * (int64_t)(w0 + warp) + (from_start ? 1 : 0)) * part_floats(D);
+#pragma unroll
+                for (int z = 0; z < NR; ++z) {
+                    float sum = l[z];
+                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 4);
+                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
+                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
+                    const int rt = cc.tile * RT + 4 * z + t;
+                    if (rt >= q.n * grp) continue;
+                    float* y;
+                    float r;
+                    if (whole_tile) {
+                        y = P.out + (int64_t)(q.row0 + rt / grp) * P.ld_out + (int64_t)(cc.hk * grp + rt % grp) * D;
+                        r = sum == 0.f ? 0.f : up / sum;
+                    } else {
+                        y = mine;
+                        if (g == 0) *reinterpret_cast<float2*>(y + MAX_RT * D + 2 * (4 * z + t)) = make_float2(m[z], sum);
+                        y += (4 * z + t) * D;
+                        r = up;
+                    }
+#pragma unroll
+                    for (int n = 0; n < D / 16; ++n) {
+                        y[16 * n + g] = (o[n][z][0] + o[n][z][1]) * r;
+                        y[16 * n + 8 + g] = (o[n][z][2] + o[n][z][3]) * r;
+                    }
+                }
+                fresh = true;
+                if (!whole_tile) {
+                    if (lane == 0) parts[warp][np] = Stretch{b0, cc.d.nc, q.row0, cc.hk, cc.tile * RT, min(RT, q.n * grp - cc.tile * RT)};
+                    ++np;
+                }
+            }
+            if (u < nu - 1) cur_next<T, RT>(P, cc);
+        }
+
+        if (lane == 0) nparts[warp] = np;
     }
 
     // ---- join the partials of the CTA's warps, then those of the CTAs: all
@@ -836,14 +841,30 @@ cudaError_t decode_launch(const AttnParams& P, int sms, cudaStream_t st) {
 }
 
 // Four rows per tile where a sequence's rows of a kv head are at most that on
-// average (the codes are then read and converted once), else eight.
+// average (32 sequences of up to 4096 keys, D = 128: 46 us, with tiles of eight
+// 60), else eight (five rows: 63 us, as two tiles of four 70; D = 256: 65 each).
 template <int D>
 cudaError_t decode_rows(const AttnParams& P, int sms, cudaStream_t st) {
     return (int64_t)P.s.ntok * (P.n_q / P.c.n_kv) <= 4 * (int64_t)P.s.nseq ? decode_launch<D, 1>(P, sms, st)
                                                                             : decode_launch<D, 2>(P, sms, st);
 }
 
-constexpr int64_t PREFILL_MIN_ROWS = 64;
+// The prefill kernel gives every 128 rows of a sequence and kv head to one CTA,
+// so its time goes by waves of CTAs; this file's kernel spreads 8-row tiles over
+// all SMs whatever their number.  A prefill tile takes as long as this many
+// 8-row tiles on one SM (in halves), and whichever needs less is taken.
+// Measured, us, here / prefill, at up to so many rows per sequence and kv head
+// (two thirds of that on average): D = 128, 8 kv heads, 32 sequences of up to
+// 4096 keys: 16 rows 106 / 175, 48 rows 207 / 178, 128 rows 527 / 178; 8
+// sequences of up to 2048: 48 rows 37 / 50, 96 rows 64 / 50; one of 4096: 128
+// rows 46 / 88; D = 256, 4 kv heads, 8 sequences of up to 4096: 128 rows 125 /
+// 261; D = 64, 16 kv heads: 32 rows 56 / 69, 64 rows 80 / 69.
+bool prefill_wins(const AttnParams& P, int sms) {
+    const int64_t halves = P.c.d == 64 ? 9 : P.c.d == 128 ? 6 : 10;
+    const int64_t rows = (int64_t)P.s.ntok * (P.n_q / P.c.n_kv), each = (rows + P.s.nseq - 1) / P.s.nseq;
+    const int64_t ctas = P.c.n_kv * (int64_t)P.s.nseq * ((each + 127) / 128), waves = (ctas + sms - 1) / sms;
+    return 2 * P.c.n_kv * rows >= 8 * halves * sms * waves;
+}
 
 }  // namespace
 
@@ -852,10 +873,8 @@ size_t kv8_attn_workspace(int n_q, int n_kv, int d, int nseq, int ntok) {
     return COUNT_BYTES + (size_t)DEC_MAX_SMS * nc * 2 * part_floats(d) * sizeof(float);
 }
 
-// Many rows per sequence and kv head: the prefill kernel, whose tiles hold
-// 128 rows and are worth filling by half.
 cudaError_t launch_kv8_attn(const AttnParams& P, int sms, cudaStream_t st) {
-    if ((int64_t)P.s.ntok * (P.n_q / P.c.n_kv) >= PREFILL_MIN_ROWS * (int64_t)P.s.nseq) return launch_kv8_prefill(P, st);
+    if (prefill_wins(P, sms)) return launch_kv8_prefill(P, st);
     return P.c.d == 64    ? decode_rows<64>(P, sms, st)
            : P.c.d == 128 ? decode_rows<128>(P, sms, st)
                           : decode_rows<256>(P, sms, st);

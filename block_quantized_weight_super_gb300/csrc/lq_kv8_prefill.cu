@@ -19,28 +19,33 @@
 //
 // Softmax.  A thread owns a row (a tensor-memory lane).  Warps 0-3 take the
 // even tiles, 4-7 the odd ones, so each has two tiles' time for one (with one
-// group of four the tensor cores waited for it: 390 us for the 4096-token
-// prompt against 250).  A first pass over S finds the tile's maximum, a second
+// group of four the tensor cores waited for it).  A first pass over S finds the tile's maximum, a second
 // one forms the weights and writes their pieces.  The scales of a page enter
 // as one factor and one summand per 16 keys: weight = 2^(S qs ks + log2(vs /
 // 2^e0) - ref), so V is used as codes; the row sum divides the value scale out
 // again per 16 keys.  ref is the row's maximum when it was last set; it is
-// raised, and O rescaled, only when a tile exceeds it by 2^4.  It goes from
+// raised, and O rescaled, only when a tile exceeds it by 2^7.  It goes from
 // tile to tile through shared memory, right after the first pass; the sums of
 // the two groups are joined at the end.
 //
 // Rounding.  The tensor cores truncate when they add to an accumulator, which
-// over thousands of keys shrinks O by 2e-8 per MMA (7e-6 after 3000 keys).  So O
-// starts anew every G tiles (64 MMAs; error 1e-6, at 5 % of the time), and the softmax threads add it up in
-// fp32: in shared memory, or for D = 256, where there is no room, in the output
-// rows.
+// over thousands of keys shrinks O by 2e-8 per MMA (7e-6 after 3000 keys).  So
+// O starts anew every G tiles (64 MMAs; error 1e-6, at 5 % of the time), and
+// the softmax threads add it up in fp32: in shared memory, or for D = 256, where
+// there is no room, in the output rows.
 //
 // Warps.  0-7 softmax, 8-11 converters: each takes the codes of 16-key groups
 // (one page each) of a tile from global memory through registers, a tile
-// ahead, into fp16 in the MMA's core-matrix layout; 12 issues S, 13 PV
-// (one thread for both spent as long on waits and commits as on the MMAs).
-// While PV(j) and then S(j + 2), which takes its place, run, the softmax works
-// on tile j + 1.
+// ahead, into fp16 in the MMA's core-matrix layout; 12 issues S, 13 PV (one
+// thread for both waited for one product while it could have issued the
+// other: 369 us for a 4096-token prompt against 356).  While PV(j) and then
+// S(j + 2), which takes its place, run, the softmax works on tile j + 1.
+//
+// Measured: 4096 tokens of 32 query and 8 kv heads, D = 128: 355 us, 387
+// TFLOP/s of the causal half, that is 775 of two-piece MMAs; the tensor cores
+// are busy a third of the time.  Bound by the chain S -> softmax -> PV -> S of
+// two tiles in flight (no room in tensor memory for a third) and by what each
+// CTA does once: 13,000 clocks until the first product, 5,000 after the last.
 //
 // Every wait is bounded: on a timeout a role records it and leaves its loop;
 // the MMAs in flight end (bounded) before the tensor memory is freed.
@@ -53,19 +58,19 @@ constexpr int PF_ROWS = 128;
 constexpr int PF_SOFT = 8, PF_CONV = 4;                      // softmax, converter warps
 constexpr int PF_MMA_WARP = PF_SOFT + PF_CONV;               // issues S; the next one issues PV
 constexpr int PF_THREADS = (PF_MMA_WARP + 2) * 32;
-// Weights are 2^(u - ref + 11), at most 2^15: the lo pieces' floor of 2^-25 is
-// 2^-36 of the row's largest weight or less.
+// Weights are 2^(u - ref + PF_SHIFT) with u - ref up to PF_RAISE, so at most
+// 2^15; the lo pieces' floor of 2^-25 is 2^-33 of the reference's weight.
 constexpr float PF_SHIFT = 8.f;
 constexpr float PF_RAISE = 7.f;
-constexpr int PF_NK = 128, PF_G = 4;
 
 template <int D>
 struct Pf {
-    static constexpr int NK = D == 256 ? 64 : PF_NK;         // keys of a tile
-    static constexpr int NB = D == 256 ? 2 : 256 / PF_NK;              // tiles in flight: S buffers, K and V stages
+    // keys of a tile (D = 128 with 64 keys and four buffers was slower)
+    static constexpr int NK = D == 256 ? 64 : 128;
+    static constexpr int NB = 2;                             // tiles in flight: S buffers, K and V stages
     static constexpr int NG = NK / 16;                       // 16-key groups
     static constexpr int GPW = NG / PF_CONV;                 // groups of a converter warp
-    static constexpr int G = D == 256 ? 8 : PF_G;                              // tiles between two flushes of O (even: warps 0-3 do them)
+    static constexpr int G = D == 256 ? 8 : 4;               // tiles between two flushes of O (even: warps 0-3 do them)
     static constexpr bool QLO_SMEM = D == 256;
     static constexpr uint32_t KB = NK * D * 2;               // bytes of a K or V tile
     static constexpr uint32_t K_OFF = 0, V_OFF = NB * KB, Q_OFF = 2 * NB * KB;
@@ -77,9 +82,8 @@ struct Pf {
     // tensor memory columns
     static constexpr uint32_t T_S = 0, T_O = NB * NK, T_QH = T_O + D, T_QL = T_QH + D / 2;
     static_assert(T_QH + (QLO_SMEM ? D / 2 : D) <= 512, "tensor memory");
-    // q's pieces on their way: hi of row w in the last two K stages, lo in the last two V stages; D = 256: hi in the last
-    // K and the last V stage
-    static constexpr int Q_STAGE = D == 256 || NB == 2 ? 1 : NB - 2;    // the first of them
+    // q's pieces on their way: hi of row w in the last K stage, lo in the last V stage; D = 256: hi in both
+    static constexpr int Q_STAGE = NB - 1;
     __device__ static constexpr uint32_t stage_hi(int w) {
         return D == 256 && w >= 64 ? V_OFF + KB + (w - 64) * D * 2 : K_OFF + Q_STAGE * KB + w * D * 2;
     }
@@ -132,9 +136,9 @@ __device__ __forceinline__ void t_wait32(uint32_t (&v)[32]) {
                  : LQ_W8(v, 0), LQ_W8(v, 8), LQ_W8(v, 16), LQ_W8(v, 24)::"memory");
 }
 // f(c, v) for the 32-column pieces c, c + 32 .. of N columns from `a` on.
-// Rolled: the loops of the roles share the instruction cache (unrolled
-// fully, with a piece on its way while another is worked on, a 4096-token prompt
-// took 487 us instead of 397).
+// Rolled: the loops of the roles share the instruction cache (unrolled fully,
+// with a piece on its way while another is worked on, a 4096-token prompt took
+// 487 us instead of the 397 of that version).
 template <int N, class F>
 __device__ __forceinline__ void t_each32(uint32_t a, F f) {
 #pragma unroll 1
