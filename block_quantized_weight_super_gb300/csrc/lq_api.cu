@@ -15,6 +15,7 @@
 #include "lq_codec.cuh"
 #include "lq_gv.cuh"
 #include "lq_internal.h"
+#include "lq_kv_internal.h"
 
 namespace lq {
 
@@ -154,7 +155,7 @@ int dev_info(DevInfo** out) {
 
 }  // namespace
 
-// The same for the entry points of other files (lq_internal.h).
+// The same for the entry points of other files (lq_kv_internal.h).
 int api_fail(int code, const char* fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
@@ -571,7 +572,7 @@ int tensor_map(CUtensorMap* out, const void* base, int64_t rows, int64_t rowbyte
 
 }  // namespace
 
-// A tensor map over bytes [d2][d1][d0] with boxes of [1][b1][b0] (lq_internal.h).
+// A tensor map over bytes [d2][d1][d0] with boxes of [1][b1][b0] (lq_kv_internal.h).
 int api_byte_map(CUtensorMap* out, const void* base, int64_t d0, int64_t d1, int64_t d2, int b0, int b1) {
     std::lock_guard<std::mutex> lk(g_map_mu);
     if (!g_encode) {

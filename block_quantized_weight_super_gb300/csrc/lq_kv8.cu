@@ -1,6 +1,6 @@
 // lq_kv8.cu -- writing the 8-bit KV cache: append (quantise new rows) and
 // page copies.
-#include "lq_internal.h"
+#include "lq_kv_internal.h"
 #include "lq_kv.cuh"
 
 namespace lq {

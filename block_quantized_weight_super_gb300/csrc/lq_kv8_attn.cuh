@@ -3,7 +3,7 @@
 #pragma once
 #include <cuda_fp16.h>
 
-#include "lq_internal.h"
+#include "lq_kv_internal.h"
 #include "lq_kv.cuh"
 
 namespace lq {

@@ -4,7 +4,7 @@
 #include <cmath>
 
 #include "../../include/lq.h"
-#include "lq_internal.h"
+#include "lq_kv_internal.h"
 #include "lq_kv.cuh"
 
 using namespace lq;

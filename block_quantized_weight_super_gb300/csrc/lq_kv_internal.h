@@ -1,0 +1,81 @@
+// lq_kv_internal.h -- declarations between the entry points and the kernels of
+// the positions, the KV cache and the attention.
+#pragma once
+#include "lq_internal.h"
+#include "lq_kv.cuh"
+
+namespace lq {
+
+// Rotary positions, the 8-bit KV cache and its attention: what lq_kv_api.cu
+// launches (lq_rope.cu, lq_kv8.cu, lq_kv_pages.cu, lq_kv8_decode.cu,
+// lq_kv8_prefill.cu).
+struct RopeParams {
+    const float* q;
+    const float* k;
+    float* qo;
+    float* ko;
+    int64_t ld_q, ld_k, ld_qo, ld_ko;
+    int32_t n_q, n_k, d, rot, adjacent, n_axes, ntok;
+    const int32_t* pos;      // [n_axes][ntok]
+    const uint8_t* axis;     // [rot / 2] or null
+    const double* freq;      // [rot / 2] radians per position
+    unsigned* status;
+};
+cudaError_t launch_rope(const RopeParams& P, int sms, cudaStream_t st);
+
+cudaError_t launch_kv8_append(const KvView& C, const KvStep& S, const float* k, int64_t ld_k, const float* v,
+                              int64_t ld_v, unsigned* status, cudaStream_t st);
+constexpr int KV_MAX_LAYERS = 64;        // layers of one copy launch
+struct KvLayers {
+    int8_t* k[KV_MAX_LAYERS];
+    int8_t* v[KV_MAX_LAYERS];
+    float* ks[KV_MAX_LAYERS];
+    float* vs[KV_MAX_LAYERS];
+};
+cudaError_t launch_kv8_copy(const KvLayers& L, int n_layers, const int32_t* src, const int32_t* dst, int n,
+                            const int32_t* count, int64_t n_pages, int n_kv, int64_t units, unsigned* status,
+                            cudaStream_t st);
+
+struct AttnParams {
+    KvView c;
+    KvStep s;
+    const float* q;
+    float* out;
+    int64_t ld_q, ld_out;
+    int32_t n_q, window;
+    float scale, softcap;
+    const int32_t* prefix;   // [nseq] or null
+    const float* slopes;     // [n_q] or null
+    uint8_t* ws;
+    uint64_t timeout_ns;
+    unsigned* status;
+};
+size_t kv8_attn_workspace(int n_q, int n_kv, int d, int nseq, int ntok);
+cudaError_t launch_kv8_attn(const AttnParams& P, int sms, cudaStream_t st);
+cudaError_t launch_kv8_prefill(const AttnParams& P, cudaStream_t st);     // lq_kv8_prefill.cu
+
+cudaError_t launch_kv_reserve(int32_t* table, int max_pages, int32_t* ref, int n_pages, int pshift, const int32_t* start,
+                              const int32_t* cu, int nseq, int32_t* info, cudaStream_t st);
+cudaError_t launch_kv_fork(int32_t* table, int n_rows, int max_pages, int32_t* ref, int n_pages, int pshift,
+                           int32_t* lens, const int32_t* parent, const int32_t* child, int n, int32_t* src, int32_t* dst,
+                           int32_t* info, unsigned* status, cudaStream_t st);
+cudaError_t launch_kv_release(int32_t* table, int n_rows, int max_pages, int32_t* ref, int n_pages, int32_t* lens,
+                              const int32_t* rows, int n, unsigned* status, cudaStream_t st);
+cudaError_t launch_kv_compact(int32_t* table, int n_rows, int max_pages, int32_t* ref, int n_pages, int32_t* map,
+                              int32_t* src, int32_t* dst, int32_t* info, unsigned* status, cudaStream_t st);
+
+// What the entry points outside lq_api.cu share with it: the calling thread's
+// error text and the current device's facts.
+struct ApiDevice {
+    int sms;
+    unsigned* status;
+    uint64_t timeout_ns;
+};
+int api_fail(int code, const char* fmt, ...);
+int api_cuda_fail(cudaError_t e, const char* what);
+void api_clear();
+int api_device(ApiDevice* out);          // an lq_status
+// a tensor map over bytes [d2][d1][d0], boxes of [1][b1][b0] (an lq_status)
+int api_byte_map(CUtensorMap* out, const void* base, int64_t d0, int64_t d1, int64_t d2, int b0, int b1);
+
+}  // namespace lq

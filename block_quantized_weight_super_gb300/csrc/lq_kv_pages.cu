@@ -10,7 +10,7 @@
 // free pages (nothing is changed otherwise), then to hand them out; it stops
 // at the last page needed.  A tile costs about a microsecond, and a request
 // is found by bisection of the requests' prefix sums in shared memory.
-#include "lq_internal.h"
+#include "lq_kv_internal.h"
 #include "lq_kv.cuh"
 
 namespace lq {

@@ -8,7 +8,7 @@
 // 32 bits is accurate to fp32 rounding.  The fp64 arithmetic, which runs at a
 // sixty-fourth of the fp32 rate, is needed once per block and pair.  The
 // kernel is bound by the memory traffic, 8 bytes per element.
-#include "lq_internal.h"
+#include "lq_kv_internal.h"
 #include "lq_kv.cuh"
 
 #include <math_constants.h>
