@@ -255,9 +255,11 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
         }
         return;
     }
-    // the reference of the value scales
-    const int pe = att_page(P, s, key0(0));
-    const int e0 = pe >= 0 ? att_e0(__ldg(P.c.vs + (int64_t)pe * P.c.n_kv + hk)) : 0;
+    // the reference of the value scales (two dependent loads: where it is needed)
+    auto scale_ref = [&]() {
+        const int pe = att_page(P, s, key0(0));
+        return pe >= 0 ? att_e0(__ldg(P.c.vs + (int64_t)pe * P.c.n_kv + hk)) : 0;
+    };
 
     if (tid == 0) {
         for (int i = 0; i < F::NB; ++i) {
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
         {
             const bool vec = ((reinterpret_cast<uintptr_t>(P.q) | (uintptr_t)(P.ld_q * 4)) & 15) == 0;
             constexpr int RW = D == 64 ? 2 : 1, NP = D == 256 ? 2 : 1;       // rows of a load, loads of a row
-            constexpr int NR = PF_ROWS / PF_SOFT, NY = 8;                    // rows of a warp; loads of rows in flight
+            constexpr int NR = PF_ROWS / PF_SOFT, NY = D == 128 ? 16 : 8;     // rows of a warp; loads of rows in flight
 #pragma unroll 1
             for (int y0 = 0; y0 < NR; y0 += NY * RW) {
                 float4 v[NY][NP];
@@ -539,6 +541,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
             ok = ok && pf_wait(&fin[w4], 0, P.timeout_ns) && pf_wait(&o_done, 0, P.timeout_ns);
             if (ok) {
                 t_after();
+                const int e0 = scale_ref();
                 const float ref = *(volatile float*)&refs[r], lr1 = *(volatile float*)&lrodd[r], l1 = *(volatile float*)&lodd[r];
                 if (lref != ref) l *= lref == -INFINITY ? 0.f : att_ex2(lref - ref);
                 l += lr1 == ref ? l1 : l1 * (lr1 == -INFINITY ? 0.f : att_ex2(lr1 - ref));
@@ -598,7 +601,6 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
         constexpr int GPW = F::GPW, NKU = D / 32, NVU = D / 32;    // 16-byte pieces per lane of a group's K, of its V
         const int pmask = (1 << P.c.pshift) - 1;
         const int64_t blk = (int64_t)D << P.c.pshift;
-        const float is = att_pow2(-e0);
         uint4 kr[GPW][NKU], vr[GPW][NVU];
         float ks[GPW], vs[GPW];
         int pg[GPW], pnext[GPW];
@@ -648,6 +650,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
         for (int x = 0; x < GPW; ++x) pg[x] = page(0, g0 + x);
         load_k(0);
         load_v(0);
+        const float is = att_pow2(-scale_ref());
 #pragma unroll
         for (int x = 0; x < GPW; ++x) pnext[x] = page(1, g0 + x);
         for (int j = 0; j < nt; ++j) {
