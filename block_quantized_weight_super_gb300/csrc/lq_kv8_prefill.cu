@@ -74,7 +74,7 @@ struct Pf {
     static constexpr bool QLO_SMEM = D == 256;
     static constexpr uint32_t KB = NK * D * 2;               // bytes of a K or V tile
     static constexpr uint32_t K_OFF = 0, V_OFF = NB * KB, Q_OFF = 2 * NB * KB;
-    static constexpr bool SUM_SMEM = D <= 128;               // where flushed O goes: [D][rows] fp32, or the output
+    static constexpr bool SUM_SMEM = D <= 128;               // where flushed O goes: [D / 4][rows][4] fp32, or the output
     static constexpr uint32_t SUM_OFF = Q_OFF + (QLO_SMEM ? PF_ROWS * D * 2 : 0);
     static constexpr uint32_t META_OFF = SUM_OFF + (SUM_SMEM ? PF_ROWS * D * 4 : 0);
     // (ks, log2, 1 / rel) of the groups of 8 tiles; and one CTA per SM, as each takes all of the tensor memory
@@ -181,12 +181,6 @@ __device__ __forceinline__ float4 lds4(uint32_t a) {
     return v;
 }
 
-__device__ __forceinline__ float pf_lds(uint32_t a) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ void pf_sts(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
 __device__ __forceinline__ void pf_st4(float* y, float4 o, bool vec) {
     if (vec) {
         *reinterpret_cast<float4*>(y) = o;
@@ -379,7 +373,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
         float sref = -INFINITY;                               // the one that the flushed O is in
         float* const yrow = P.out + qrow * P.ld_out + (int64_t)head * D;
         const bool ovec = ((reinterpret_cast<uintptr_t>(P.out) | (uintptr_t)(P.ld_out * 4)) & 15) == 0;
-        const uint32_t sum = sbase + F::SUM_OFF + r * 4;
+        const uint32_t sum = sbase + F::SUM_OFF + r * 16;
         // Where this row's flushed column c + e lies in the output rows: 32 x 32
         // blocks transposed, so that a warp's access is one line (rows of an
         // incomplete block: in place).
@@ -498,16 +492,17 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
                 } else if (F::SUM_SMEM) {
                     t_each32<D>(trow + F::T_O, [&](int c, uint32_t (&v)[32]) {
                         // (all loads before the first store: they could not pass it)
-                        float z[32];
-                        if (more) {
+                        float4 z[8];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) z[e] = pf_lds(sum + (c + e) * (PF_ROWS * 4)) * gs;
-                        } else {
+                        for (int e = 0; e < 8; ++e) z[e] = more ? lds4(sum + (c / 4 + e) * (PF_ROWS * 16)) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) z[e] = 0.f;
+                        for (int e = 0; e < 8; ++e) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                w[k] = __float_as_uint(fmaf(__uint_as_float(v[4 * e + k]), f, (k == 0 ? z[e].x : k == 1 ? z[e].y : k == 2 ? z[e].z : z[e].w) * gs));
+                            sts128(sum + (c / 4 + e) * (PF_ROWS * 16), w[0], w[1], w[2], w[3]);
                         }
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) pf_sts(sum + (c + e) * (PF_ROWS * 4), fmaf(__uint_as_float(v[e]), f, z[e]));
                     });
                 } else {
                     t_each32<D>(trow + F::T_O, [&](int c, uint32_t (&v)[32]) {
@@ -562,8 +557,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
                         if (more) {
                             float4 z;
                             if (F::SUM_SMEM) {
-                                const uint32_t a = sum + (c + e) * (PF_ROWS * 4);
-                                z = make_float4(pf_lds(a), pf_lds(a + PF_ROWS * 4), pf_lds(a + 2 * PF_ROWS * 4), pf_lds(a + 3 * PF_ROWS * 4));
+                                z = lds4(sum + ((c + e) >> 2) * (PF_ROWS * 16));
                             } else {
                                 const float *y0 = out_slot(c, e), *y1 = out_slot(c, e + 1), *y2 = out_slot(c, e + 2), *y3 = out_slot(c, e + 3);
                                 z = rok ? make_float4(*y0, *y1, *y2, *y3) : make_float4(0.f, 0.f, 0.f, 0.f);
