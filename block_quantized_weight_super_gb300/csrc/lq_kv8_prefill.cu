@@ -70,7 +70,7 @@ struct Pf {
     static constexpr int NB = 2;                             // tiles in flight: S buffers, K and V stages
     static constexpr int NG = NK / 16;                       // 16-key groups
     static constexpr int GPW = NG / PF_CONV;                 // groups of a converter warp
-    static constexpr int G = D == 256 ? 8 : 4;               // tiles between two flushes of O (even: warps 0-3 do them)
+    static constexpr int G = D == 256 ? 8 : 4;               // tiles between two flushes of O
     static constexpr bool QLO_SMEM = D == 256;
     static constexpr uint32_t KB = NK * D * 2;               // bytes of a K or V tile
     static constexpr uint32_t K_OFF = 0, V_OFF = NB * KB, Q_OFF = 2 * NB * KB;
@@ -209,8 +209,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
     constexpr int NK = F::NK, NG = F::NG, NB = F::NB;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t k_full[F::NB], k_free[F::NB], v_full[F::NB], v_free[F::NB], s_full[F::NB], p_full[F::NB], q_full, o_done;
-    __shared__ uint64_t ref_full[4], fin[4];                 // per warp of rows: a tile's reference is out; the odd tiles are done
-    __shared__ float refs[PF_ROWS], lodd[PF_ROWS], lrodd[PF_ROWS], qscale[PF_ROWS];
+    __shared__ uint64_t pair[4];                             // the two warps of 32 rows
+    __shared__ float xch[2][2][PF_ROWS], qscale[PF_ROWS];    // what they tell each other: [tile & 1][group][row]
     __shared__ uint32_t tslot;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int grp = P.n_q / P.c.n_kv, hk = blockIdx.y;
@@ -262,12 +262,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
             mbar_init(&k_free[i], 1);
             mbar_init(&v_free[i], 1);
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[i], PF_SOFT);
         }
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(&ref_full[i], 1);
-            mbar_init(&fin[i], 1);
-        }
+        for (int i = 0; i < 4; ++i) mbar_init(&pair[i], 2);
         mbar_init(&o_done, 1);
         mbar_init(&q_full, PF_SOFT);
         fence_mbar_init();
@@ -286,7 +283,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
     const uint32_t sbase = smem_u32(smem), meta = sbase + F::META_OFF;
 
     if (warp < PF_SOFT) {
-        // ---- softmax: thread = row, warps 0-3 even tiles, 4-7 odd ones
+        // ---- softmax: thread = row, warps 0-3 the first half of a tile's keys and of O's columns, 4-7 the second
+        constexpr int NH = NK / 2, DH = D / 2;
         const int wg = warp >> 2, w4 = warp & 3, r = w4 * 32 + lane;
         const bool rok = r < rows;
         int head;
@@ -369,11 +367,21 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
         t_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full);
-        float l = 0.f, lref = -INFINITY;                      // this group's sum, and the reference that it is in
+        float l = 0.f, ref = -INFINITY;                       // the sum of this half's weights, the reference
         float sref = -INFINITY;                               // the one that the flushed O is in
-        float* const yrow = P.out + qrow * P.ld_out + (int64_t)head * D;
+        // What the row's other thread says for the same i (0, 1, ...).
+        auto exchange = [&](int i, float& x) -> bool {
+            volatile float* const y = &xch[i & 1][0][r];
+            y[wg * PF_ROWS] = x;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pair[w4]);
+            if (!pf_wait(&pair[w4], (uint32_t)i & 1, P.timeout_ns)) return false;
+            x = y[(wg ^ 1) * PF_ROWS];
+            return true;
+        };
+        float* const yrow = P.out + qrow * P.ld_out + (int64_t)head * D + wg * DH;
         const bool ovec = ((reinterpret_cast<uintptr_t>(P.out) | (uintptr_t)(P.ld_out * 4)) & 15) == 0;
-        const uint32_t sum = sbase + F::SUM_OFF + r * 16;
+        const uint32_t sum = sbase + F::SUM_OFF + wg * (DH / 4) * (PF_ROWS * 16) + r * 16;
         // Where this row's flushed column c + e lies in the output rows: 32 x 32
         // blocks transposed, so that a warp's access is one line (rows of an
         // incomplete block: in place).
@@ -382,18 +390,19 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
             const uint64_t y = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(yrow), e);
             return block ? reinterpret_cast<float*>(y) + c + lane : yrow + c + e;
         };
-        for (int j = wg; j < nt; j += 2) {
-            const int k0 = key0(j);
-            const uint32_t ts = trow + F::T_S + (j % NB) * NK, mt = meta + (j & 7) * NG * 16;
+        const uint32_t to = trow + F::T_O + wg * DH;
+        for (int j = 0; j < nt; ++j) {
+            const int k0 = key0(j) + wg * NH;
+            const uint32_t ts = trow + F::T_S + (j % NB) * NK + wg * NH, mt = meta + (j & 7) * NG * 16 + wg * NH;
             if (!(ok = pf_wait(&s_full[j % NB], (uint32_t)(j / NB) & 1, P.timeout_ns))) break;
             t_after();
-            const bool whole = k0 + NK <= vpre || (k0 >= vlo && k0 + NK <= vhi);
+            const bool whole = k0 + NH <= vpre || (k0 >= vlo && k0 + NH <= vhi);
             const bool plain = !EXTRA && __all_sync(0xFFFFFFFFu, whole);
             // pass 1: the maximum (and, where the scores are more than one
             // multiply-add of S, the finished exponents back in place of S)
             float mx = -INFINITY;
             if (plain) {
-                t_each32<NK>(ts, [&](int c, uint32_t (&v)[32]) {
+                t_each32<NH>(ts, [&](int c, uint32_t (&v)[32]) {
                     const float4 m0 = lds4(mt + c), m1 = lds4(mt + c + 16);
                     float a[4];
 #pragma unroll
@@ -406,7 +415,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
                 });
             } else {
 #pragma unroll 1
-                for (int c = 0; c < NK; c += 32) {
+                for (int c = 0; c < NH; c += 32) {
                     uint32_t v[32];
                     t_ld32(ts + c, v);
                     const float4 m0 = lds4(mt + c), m1 = lds4(mt + c + 16);
@@ -430,24 +439,19 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
                 }
             }
             if (!plain) t_wait_st();
-            // the reference: the last tile's, or raised
-            float before = -INFINITY;
-            if (j > 0) {
-                if (!(ok = pf_wait(&ref_full[w4], (uint32_t)(j - 1) & 1, P.timeout_ns))) break;
-                before = *(volatile float*)&refs[r];
-            }
+            // the reference: the last tile's, or raised to the maximum of both
+            // halves (both threads of a row come to the same)
+            const float before = ref;
+            float other = mx;
+            if (!(ok = exchange(j, other))) break;
+            mx = fmaxf(mx, other);
             const bool raise = mx > before + PF_RAISE || (before == -INFINITY && mx > -INFINITY);
-            const float ref = raise ? mx : before;
-            *(volatile float*)&refs[r] = ref;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ref_full[w4]);
-            if (lref != ref) {
-                l *= lref == -INFINITY ? 0.f : att_ex2(lref - ref);
-                lref = ref;
-            }
+            const float down = !raise ? 1.f : before == -INFINITY ? 0.f : att_ex2(before - mx);
+            if (raise) ref = mx;
+            l *= down;
             // pass 2: weights, their sums per 16 keys, their pieces
             const float sub = ref == -INFINITY ? 0.f : ref - PF_SHIFT;
-            t_each32<NK>(ts, [&](int c, uint32_t (&v)[32]) {
+            t_each32<NH>(ts, [&](int c, uint32_t (&v)[32]) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {                 // 16 keys: hi pieces in 8 columns, lo pieces in the next 8
                     const float4 mm = lds4(mt + c + 16 * h);
@@ -479,18 +483,18 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
             if (j > 0 && (flush || __any_sync(0xFFFFFFFFu, raise))) {
                 if (!(ok = pf_wait(&v_free[(j - 1) % NB], (uint32_t)((j - 1) / NB) & 1, P.timeout_ns))) break;
                 t_after();
-                const float f = raise ? (before == -INFINITY ? 0.f : att_ex2(before - ref)) : 1.f;
+                const float f = down;
                 const bool more = j > F::G;                   // there is a sum from earlier flushes
                 const float gs = sref == -INFINITY ? 0.f : att_ex2(sref - ref);
                 if (flush) sref = ref;
                 if (!flush) {
-                    t_each32<D>(trow + F::T_O, [&](int c, uint32_t (&v)[32]) {
+                    t_each32<DH>(to, [&](int c, uint32_t (&v)[32]) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-                        t_st32(trow + F::T_O + c, v);
+                        t_st32(to + c, v);
                     });
                 } else if (F::SUM_SMEM) {
-                    t_each32<D>(trow + F::T_O, [&](int c, uint32_t (&v)[32]) {
+                    t_each32<DH>(to, [&](int c, uint32_t (&v)[32]) {
                         // (all loads before the first store: they could not pass it)
                         float4 z[8];
 #pragma unroll
@@ -505,7 +509,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
                         }
                     });
                 } else {
-                    t_each32<D>(trow + F::T_O, [&](int c, uint32_t (&v)[32]) {
+                    t_each32<DH>(to, [&](int c, uint32_t (&v)[32]) {
                         float z[32];
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
@@ -525,30 +529,24 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[j % NB]);
         }
-        if (wg == 1) {
-            *(volatile float*)&lodd[r] = l;
-            *(volatile float*)&lrodd[r] = lref;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&fin[w4]);
-        } else {
-            // ---- output.  (The last PV has a barrier of its own: which phase
-            // v_free is in by now is not known, and a parity does not tell.)
-            ok = ok && pf_wait(&fin[w4], 0, P.timeout_ns) && pf_wait(&o_done, 0, P.timeout_ns);
+        // ---- output.  (The last PV has a barrier of its own: which phase
+        // v_free is in by now is not known, and a parity does not tell.)
+        {
+            float other = l;
+            ok = ok && exchange(nt, other) && pf_wait(&o_done, 0, P.timeout_ns);
             if (ok) {
                 t_after();
                 const int e0 = scale_ref();
-                const float ref = *(volatile float*)&refs[r], lr1 = *(volatile float*)&lrodd[r], l1 = *(volatile float*)&lodd[r];
-                if (lref != ref) l *= lref == -INFINITY ? 0.f : att_ex2(lref - ref);
-                l += lr1 == ref ? l1 : l1 * (lr1 == -INFINITY ? 0.f : att_ex2(lr1 - ref));
+                l += other;
                 const float gs = sref == -INFINITY ? 0.f : att_ex2(sref - ref);
                 const bool more = nt > F::G;
                 const float f = l == 0.f ? 0.f : att_pow2(e0) / l;
                 // through shared memory (the K and V buffers, free by now), so
                 // that a warp stores whole rows
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
+                for (int c = 0; c < DH; c += 32) {
                     uint32_t v[32];
-                    t_ld32(trow + F::T_O + c, v);
+                    t_ld32(to + c, v);
                     t_wait32(v);
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
@@ -565,7 +563,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kv8_prefill_kernel(const __grid
                             o = pf_fma4(z, gs, o);
                         }
                         if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
-                        const uint32_t a = sbase + r * (D * 4) + ((((c + e) >> 2) ^ (r & 7)) << 4);
+                        const uint32_t a = sbase + r * (D * 4) + (((wg * (DH / 4) + ((c + e) >> 2)) ^ (r & 7)) << 4);
                         sts128(a, __float_as_uint(o.x * f), __float_as_uint(o.y * f), __float_as_uint(o.z * f), __float_as_uint(o.w * f));
                     }
                 }
