@@ -17,16 +17,17 @@
 // (D = 256 has no room there for the lo pieces of Q: those stay in shared
 // memory.)
 //
-// Softmax.  A thread owns a row (a tensor-memory lane).  Warps 0-3 take the
-// even tiles, 4-7 the odd ones, so each has two tiles' time for one (with one
-// group of four the tensor cores waited for it).  A first pass over S finds the tile's maximum, a second
-// one forms the weights and writes their pieces.  The scales of a page enter
-// as one factor and one summand per 16 keys: weight = 2^(S qs ks + log2(vs /
-// 2^e0) - ref), so V is used as codes; the row sum divides the value scale out
-// again per 16 keys.  ref is the row's maximum when it was last set; it is
-// raised, and O rescaled, only when a tile exceeds it by 2^7.  It goes from
-// tile to tile through shared memory, right after the first pass; the sums of
-// the two groups are joined at the end.
+// Softmax.  Two threads share a row (a tensor-memory lane): warps 0-3 have the
+// first half of a tile's keys and of O's columns, 4-7 the second.  (With the
+// two groups on alternate tiles, whole rows each, a 4096-token prompt took 338
+// us instead of 326: a tile's softmax is twice as long then, and two tiles in
+// flight do not hide it.)  A first pass over S finds the tile's maximum, which
+// the two tell each other through shared memory; a second one forms the weights
+// and writes their pieces.  The scales of a page enter as one factor and one
+// summand per 16 keys: weight = 2^(S qs ks + log2(vs / 2^e0) - ref), so V is
+// used as codes; the row sum divides the value scale out again per 16 keys.  ref
+// is the row's maximum when it was last set; it is raised, and O rescaled, only
+// when a tile exceeds it by 2^7.
 //
 // Rounding.  The tensor cores truncate when they add to an accumulator, which
 // over thousands of keys shrinks O by 2e-8 per MMA (7e-6 after 3000 keys).  So
@@ -41,11 +42,11 @@
 // other: 369 us for a 4096-token prompt against 356).  While PV(j) and then
 // S(j + 2), which takes its place, run, the softmax works on tile j + 1.
 //
-// Measured: 4096 tokens of 32 query and 8 kv heads, D = 128: 355 us, 387
-// TFLOP/s of the causal half, that is 775 of two-piece MMAs; the tensor cores
-// are busy a third of the time.  Bound by the chain S -> softmax -> PV -> S of
+// Measured: 4096 tokens of 32 query and 8 kv heads, D = 128: 314 us, 440
+// TFLOP/s of the causal half, that is 880 of two-piece MMAs; the tensor cores
+// are busy two fifths of the time.  Bound by the chain S -> softmax -> PV -> S of
 // two tiles in flight (no room in tensor memory for a third) and by what each
-// CTA does once: 13,000 clocks until the first product, 5,000 after the last.
+// CTA does once: 10,000 clocks until the first product, 4,000 after the last.
 //
 // Every wait is bounded: on a timeout a role records it and leaves its loop;
 // the MMAs in flight end (bounded) before the tensor memory is freed.
@@ -195,12 +196,10 @@ __device__ __forceinline__ float4 pf_fma4(float4 a, float b, float4 c) {
     return make_float4(fmaf(a.x, b, c.x), fmaf(a.y, b, c.y), fmaf(a.z, b, c.z), fmaf(a.w, b, c.w));
 }
 
-// Lane 0 waits (32 lanes polling one barrier serialise on it), the warp follows.
+// The whole warp waits.  (One lane for all, its result handed on by a shuffle,
+// lengthened the chain of waits: a 4096-token prompt took 326 us instead of 307.)
 __device__ __forceinline__ bool pf_wait(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
-    bool ok = true;
-    if ((threadIdx.x & 31) == 0) ok = att_wait(bar, parity, timeout_ns);
-    __syncwarp();
-    return __shfl_sync(0xFFFFFFFFu, ok, 0);
+    return __all_sync(0xFFFFFFFFu, att_wait(bar, parity, timeout_ns));
 }
 
 template <int D, bool EXTRA>
