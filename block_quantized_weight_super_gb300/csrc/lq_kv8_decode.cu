@@ -854,13 +854,14 @@ cudaError_t decode_rows(const AttnParams& P, int sms, cudaStream_t st) {
 // all SMs whatever their number.  A prefill tile takes as long as this many
 // 8-row tiles on one SM (in halves), and whichever needs less is taken.
 // Measured, us, here / prefill, at up to so many rows per sequence and kv head
-// (two thirds of that on average): D = 128, 8 kv heads, 32 sequences of up to
-// 4096 keys: 16 rows 106 / 175, 48 rows 207 / 178, 128 rows 527 / 178; 8
-// sequences of up to 2048: 48 rows 37 / 50, 96 rows 64 / 50; one of 4096: 128
-// rows 46 / 88; D = 256, 4 kv heads, 8 sequences of up to 4096: 128 rows 125 /
-// 261; D = 64, 16 kv heads: 32 rows 56 / 69, 64 rows 80 / 69.
+// (two thirds of that on average where there are several sequences): D = 128, 8
+// kv heads, 32 sequences of up to 4096 keys: 16 rows 106 / 157, 32 rows 192 /
+// 158, 128 rows 525 / 159; 8 sequences of up to 2048: 48 rows 37 / 43, 64 rows
+// 53 / 43; one of 4096: 128 rows 46 / 77, 256 rows 74 / 77; D = 256, 4 kv heads,
+// 8 sequences of up to 4096: 128 rows 125 / 236; D = 64, 16 kv heads: 32 rows
+// 56 / 57, 64 rows 80 / 58.
 bool prefill_wins(const AttnParams& P, int sms) {
-    const int64_t halves = P.c.d == 64 ? 9 : P.c.d == 128 ? 6 : 10;
+    const int64_t halves = P.c.d == 64 ? 5 : P.c.d == 128 ? 4 : 9;
     const int64_t rows = (int64_t)P.s.ntok * (P.n_q / P.c.n_kv), each = (rows + P.s.nseq - 1) / P.s.nseq;
     const int64_t ctas = P.c.n_kv * (int64_t)P.s.nseq * ((each + 127) / 128), waves = (ctas + sms - 1) / sms;
     return 2 * P.c.n_kv * rows >= 8 * halves * sms * waves;

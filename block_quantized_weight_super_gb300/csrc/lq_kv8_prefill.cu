@@ -42,8 +42,8 @@
 // other: 369 us for a 4096-token prompt against 356).  While PV(j) and then
 // S(j + 2), which takes its place, run, the softmax works on tile j + 1.
 //
-// Measured: 4096 tokens of 32 query and 8 kv heads, D = 128: 314 us, 440
-// TFLOP/s of the causal half, that is 880 of two-piece MMAs; the tensor cores
+// Measured: 4096 tokens of 32 query and 8 kv heads, D = 128: 309 us, 445
+// TFLOP/s of the causal half, that is 890 of two-piece MMAs; the tensor cores
 // are busy two fifths of the time.  Bound by the chain S -> softmax -> PV -> S of
 // two tiles in flight (no room in tensor memory for a third) and by what each
 // CTA does once: 10,000 clocks until the first product, 4,000 after the last.
