@@ -75,3 +75,25 @@ def test_long_prompt(lq, d, page, n_kv, grp):  # noqa: F811
     ref, mag = (torch.einsum("hgnl,hld->hgnd", w, x).permute(2, 0, 1, 3).reshape(n, -1) for x in (V, V.abs()))
     # as for the long caches: scores below 12 in size, weights in two pieces, L / 8 sums
     assert ((out.double() - ref).abs() <= mag * (2 * 60 * 2.0 ** -21 + 2.0 ** -20 + (L / 8 + 64) * T.R.U)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("rise", [0.0, 0.02, 3.0, -3.0])
+@pytest.mark.parametrize("pad", [0, 3])
+def test_long_rows_whose_maximum_moves(lq, d, rise, pad):  # noqa: F811
+    """scores that rise, or fall, by `rise` per key over 1500 keys: the running maximum stays, moves now and then or at every step, and
+    the sums taken out of the accumulators on the way follow it; q and out rows on 16- and on 4-byte addresses"""
+    rng = np.random.default_rng(d + pad)
+    n, L, page = 90, 1500, 64
+    pages = -(-L // page)
+    c = T.R.Cache(pages, 1, page, d, rng)
+    c.ks[:] = 1.0 / 32
+    steps = np.rint(np.arange(pages * page) / (pages * page) * 254 - 127)          # dim 0 rises from -127 to 127
+    c.k[..., 0] = steps.reshape(pages, 1, page).astype(np.int8)
+    q = (rng.standard_normal((n, 2 * d)) * 0.05).astype(np.float32)
+    q[:, 0] = q[:, d] = rise * pages * page / 254 * 32
+    table = np.arange(pages, dtype=np.int32)[None]
+    got = T.run_attn(lq, c, table, [L - n], [0, n], q, 2, 1.0, pad=pad)
+    ref, bound = T.R.attn(c, table, [L - n], [0, n], q, 2, 1.0)
+    T.check(got, ref, bound, f"rise {rise}")
